@@ -6,14 +6,20 @@ loudly if the library is missing.
 """
 
 from .api import (  # noqa: F401
+    KVCache,
     Metadata,
     Schedule,
     anchor,
+    block_attn,
+    block_means,
+    block_topk,
+    cache_write,
     dense_attn,
     group,
     host_staging,
     perquery_attn,
     residual,
+    rotary,
     select,
     select_blocks,
     select_noalloc,

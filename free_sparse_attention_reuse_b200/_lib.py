@@ -36,6 +36,13 @@ EXPORTS = (
     "mcs_set_attn_wait_limit",
     "mcs_kmeans_workspace_size",
     "mcs_group_kmeans",
+    "mcs_rotary",
+    "mcs_block_means",
+    "mcs_block_topk_workspace_size",
+    "mcs_block_topk",
+    "mcs_cache_write",
+    "mcs_block_attn_workspace_size",
+    "mcs_block_attn",
 )
 
 STATUS_NAMES = {
@@ -60,6 +67,19 @@ class MCSError(RuntimeError):
 class Shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("N", ctypes.c_int), ("d", ctypes.c_int),
                 ("scale", ctypes.c_float)]
+
+
+class BlockShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("Hkv", ctypes.c_int), ("Nq", ctypes.c_int),
+                ("Nk", ctypes.c_int), ("d", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class RotaryArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("N", ctypes.c_int), ("H", ctypes.c_int), ("Hkv", ctypes.c_int),
+                ("d", ctypes.c_int), ("axes", ctypes.c_int), ("axis_dim", ctypes.c_int * 4),
+                ("theta", ctypes.c_double), ("eps", ctypes.c_float), ("pairs", ctypes.c_int),
+                ("norm", ctypes.c_int), ("pos_is_float", ctypes.c_int), ("pos_per_batch", ctypes.c_int),
+                ("weight_is_bf16", ctypes.c_int), ("stride", (ctypes.c_longlong * 3) * 3)]
 
 
 _lib = None
@@ -115,6 +135,21 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mcs_group_kmeans.argtypes = [Shape, vp, ctypes.c_int, ctypes.c_int, i32p, vp, ctypes.c_size_t, vp]
     lib.mcs_set_attn_wait_limit.restype = ctypes.c_uint64
     lib.mcs_set_attn_wait_limit.argtypes = [ctypes.c_uint64, vp]
+    ci, cz = ctypes.c_int, ctypes.c_size_t
+    lib.mcs_rotary.restype = ci
+    lib.mcs_rotary.argtypes = [ctypes.POINTER(RotaryArgs)] + [vp] * 10
+    lib.mcs_block_means.restype = ci
+    lib.mcs_block_means.argtypes = [Shape, vp, ci, i32p, vp, vp]
+    lib.mcs_block_topk_workspace_size.restype = cz
+    lib.mcs_block_topk_workspace_size.argtypes = [BlockShape, ci, ci]
+    lib.mcs_block_topk.restype = ci
+    lib.mcs_block_topk.argtypes = [BlockShape, vp, vp, ci, ci, ci, i32p, i32p, vp, cz, vp]
+    lib.mcs_cache_write.restype = ci
+    lib.mcs_cache_write.argtypes = [Shape, vp, vp, ci, ci, ci, i32p, vp, vp, vp, vp, vp, vp]
+    lib.mcs_block_attn_workspace_size.restype = cz
+    lib.mcs_block_attn_workspace_size.argtypes = [BlockShape, ci, ci, ci]
+    lib.mcs_block_attn.restype = ci
+    lib.mcs_block_attn.argtypes = [BlockShape, vp, vp, vp, ci, vp, vp, i32p, ci, ci, ci, i32p, vp, vp, vp, vp, cz, vp]
     _lib = lib
     return lib
 

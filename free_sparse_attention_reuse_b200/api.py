@@ -346,6 +346,325 @@ def group_kmeans(Q, C: int, iters: int = 10, perm=None, ws=None, scale=None):
     return perm
 
 
+# ---------------------------------------------------------------- block-sparse attention without an anchor
+E4M3 = torch.float8_e4m3fn
+BLOCK_ROWS = (32, 64, 128)      # keys of a block
+QUERY_ROWS = (1, 16, 64, 128)   # query rows that share a list
+
+
+def _heads(t, name: str, dtype=torch.bfloat16):
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        raise ValueError(f"{name} must be a 4-d tensor [B, H, N, d]")
+    _spec(t, name, dtype)
+    return tuple(t.shape)
+
+
+def _block_sizes(C=None, BK=None):
+    if BK is not None and BK not in BLOCK_ROWS:
+        raise ValueError(f"BK must be one of {BLOCK_ROWS}, got {BK!r}")
+    if C is not None and C not in QUERY_ROWS:
+        raise ValueError(f"C must be one of {QUERY_ROWS}, got {C!r}")
+
+
+def _kv_heads(H: int, Hkv: int):
+    if Hkv < 1 or H % Hkv:
+        raise ValueError(f"the {Hkv} key/value heads must divide the {H} query heads")
+
+
+def _strides(t):
+    """Element strides of [B, N, H] (0 for a dimension of one entry, whose stride means nothing)."""
+    return [0 if t.shape[i] == 1 else t.stride(i) for i in range(3)]
+
+
+def _apart(outs: dict, ins: dict):
+    """No output may share memory with an input: the kernels read inputs after they have written."""
+    def span(t):
+        n = 1 + sum((s - 1) * st for s, st in zip(t.shape, t.stride())) if t.numel() else 0
+        return t.data_ptr(), t.data_ptr() + n * t.element_size()
+
+    for a, o in outs.items():
+        if o is None:
+            continue
+        lo, hi = span(o)
+        for b, t in ins.items():
+            if t is not None and lo < span(t)[1] and span(t)[0] < hi:
+                raise ValueError(f"{a} must not share memory with {b}")
+
+
+def _length(t, name: str, B: int):
+    if t is not None:
+        _spec(t, name, torch.int32, (B,))
+
+
+def rotary(q, k, v, pos, axes, theta: float = 10000.0, pairs: str = "adjacent", norm=None, q_weight=None,
+           k_weight=None, eps: float = 1e-6, out=None):
+    """A layer's projections to attention-ready tensors in one pass: RMS norm of q and k, rotary
+    positions over several axes, and the change to head-major layout.
+
+    q [B, N, H, d], k and v [B, N, Hkv, d]: bf16 views (for example the parts of a fused projection
+    [B, N, 3, H, d]) with consecutive elements in a row; k and v may be None.  pos: int32 or fp32
+    [N, A] or [B, N, A], a token's position on each of the A axes.  axes: how many of a row's d
+    elements each axis turns (even; elements behind their sum stay).  theta: base of the
+    frequencies.  pairs: "adjacent" (elements 2i, 2i+1) or "halves" (i, i + sum(axes)/2).  norm:
+    None, "head" (over a row, weights [d]) or "token" (over all heads of a token, weights
+    [heads, d]); weights fp32 or bf16, or None for ones.  Returns Q [B, H, N, d], K and V
+    [B, Hkv, N, d] contiguous (None where the input is None); out = (Q, K, V) to reuse buffers."""
+    if pairs not in ("adjacent", "halves"):
+        raise ValueError(f"pairs must be 'adjacent' or 'halves', got {pairs!r}")
+    if norm not in (None, "head", "token"):
+        raise ValueError(f"norm must be None, 'head' or 'token', got {norm!r}")
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a 4-d tensor [B, N, H, d]")
+    B, N, H, d = q.shape
+    Hkv = H
+    for t, name in ((k, "k"), (v, "v")):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise ValueError(f"{name} must be a 4-d tensor [B, N, H, d]")
+        Hkv = t.shape[2] if name == "k" or k is None else Hkv
+        if tuple(t.shape) != (B, N, Hkv, d):
+            raise ValueError(f"{name} must have shape {(B, N, Hkv, d)}, got {tuple(t.shape)}")
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t is None:
+            continue
+        if t.dtype != torch.bfloat16:
+            raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+        if t.stride(3) != 1 or any(x % 8 for x in _strides(t)):
+            raise ValueError(f"{name} must have consecutive elements in a row and strides that are multiples of 8")
+    axes = tuple(int(a) for a in axes)
+    if not 1 <= len(axes) <= 4 or any(a < 2 or a % 2 for a in axes) or sum(axes) > d:
+        raise ValueError(f"axes must be one to four even sizes of at most {d} in all, got {axes}")
+    if pairs == "halves" and sum(axes) % 16:
+        raise ValueError("pairs='halves' needs the axes' sizes to sum to a multiple of 16")
+    if not isinstance(pos, torch.Tensor) or pos.dtype not in (torch.int32, torch.float32):
+        raise ValueError("pos must be an int32 or float32 tensor")
+    if tuple(pos.shape) not in ((N, len(axes)), (B, N, len(axes))):
+        raise ValueError(f"pos must have shape {(N, len(axes))} or {(B, N, len(axes))}, got {tuple(pos.shape)}")
+    _spec(pos, "pos", pos.dtype)
+    if norm is None and (q_weight is not None or k_weight is not None):
+        raise ValueError("norm weights need norm='head' or norm='token'")
+    wdt = None
+    for w, name, heads in ((q_weight, "q_weight", H), (k_weight, "k_weight", Hkv)):
+        if w is None:
+            continue
+        if not isinstance(w, torch.Tensor) or w.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"{name} must be a float32 or bfloat16 tensor")
+        if wdt is not None and w.dtype != wdt:
+            raise ValueError("q_weight and k_weight must have one dtype")
+        wdt = w.dtype
+        _spec(w, name, wdt, (d,) if norm == "head" else (heads, d))
+    if out is None:
+        mk = lambda h: torch.empty((B, h, N, d), dtype=torch.bfloat16, device=q.device)  # noqa: E731
+        out = (mk(H), None if k is None else mk(Hkv), None if v is None else mk(Hkv))
+    Q, K, V = out
+    for t, o, name, heads in ((q, Q, "Q", H), (k, K, "K", Hkv), (v, V, "V", Hkv)):
+        if (t is None) != (o is None):
+            raise ValueError(f"{name} must be given exactly where its input is")
+        if o is not None:
+            _spec(o, name, torch.bfloat16, (B, heads, N, d))
+    _on_device(q=q, k=k, v=v, pos=pos, q_weight=q_weight, k_weight=k_weight, Q=Q, K=K, V=V)
+    _apart(dict(Q=Q, K=K, V=V), dict(q=q, k=k, v=v))
+    a = _lib.RotaryArgs(B=B, N=N, H=H, Hkv=Hkv, d=d, axes=len(axes), theta=theta, eps=eps,
+                        pairs=int(pairs == "halves"), norm=(None, "head", "token").index(norm),
+                        pos_is_float=int(pos.dtype == torch.float32), pos_per_batch=int(pos.dim() == 3),
+                        weight_is_bf16=int(wdt == torch.bfloat16))
+    for i, x in enumerate(axes):
+        a.axis_dim[i] = x
+    for i, t in enumerate((q, k, v)):
+        if t is not None:
+            a.stride[i][:] = _strides(t)
+    check(_lib.load().mcs_rotary(a, ptr(q), ptr(k), ptr(v), ptr(pos), ptr(q_weight), ptr(k_weight), ptr(Q), ptr(K),
+                                 ptr(V), stream_ptr()), "mcs_rotary")
+    return Q, K, V
+
+
+def block_means(K, BK: int, kv_len=None, means=None):
+    """Mean of the valid rows of every block of BK rows: fp32 [B, H, ceil(N / BK), d] (zero for a
+    block without one).  kv_len: int32 [B], valid rows of each batch entry."""
+    B, H, N, d = _heads(K, "K")
+    _block_sizes(BK=BK)
+    _length(kv_len, "kv_len", B)
+    shape = (B, H, -(-N // BK), d)
+    if means is None:
+        means = torch.empty(shape, dtype=torch.float32, device=K.device)
+    _spec(means, "means", torch.float32, shape)
+    _on_device(K=K, kv_len=kv_len, means=means)
+    check(_lib.load().mcs_block_means(Shape(B, H, N, d, 0.0), ptr(K), BK, ptr(kv_len), ptr(means), stream_ptr()),
+          "mcs_block_means")
+    return means
+
+
+def block_topk(Q, means, C: int, kb: int, BK: int, kv_len=None, blocks=None, ws=None):
+    """The kb key blocks of largest pooled score for every block of C query rows: int32
+    [B, H, ceil(Nq / C), kb], ascending, -1 behind them where fewer blocks hold a valid key.
+
+    means: fp32 [B, Hkv, nb, d] from block_means or cache_write.  score = (mean of the query rows) .
+    (mean of the block's keys), ties to the lower block.  kv_len: int32 [B], valid keys; a block
+    behind them is not a candidate."""
+    B, H, Nq, d = _heads(Q, "Q")
+    Hkv, nb = _heads(means, "means", torch.float32)[1:3]
+    _spec(means, "means", torch.float32, (B, Hkv, nb, d))
+    _kv_heads(H, Hkv)
+    _block_sizes(C, BK)
+    if not 1 <= kb <= nb:
+        raise ValueError(f"kb must be in [1, {nb}], got {kb}")
+    _length(kv_len, "kv_len", B)
+    shape = (B, H, -(-Nq // C), kb)
+    if blocks is None:
+        blocks = torch.empty(shape, dtype=torch.int32, device=Q.device)
+    _spec(blocks, "blocks", torch.int32, shape)
+    _on_device(Q=Q, means=means, kv_len=kv_len, blocks=blocks)
+    lib = _lib.load()
+    s = _lib.BlockShape(B, H, Hkv, Nq, nb * BK, d, 0.0)
+    if ws is None:
+        n = int(lib.mcs_block_topk_workspace_size(s, C, BK))
+        if n == 0:
+            raise _lib.MCSError(2, "mcs_block_topk_workspace_size: invalid shape")
+        ws = torch.empty(n, dtype=torch.uint8, device=Q.device)
+    _spec(ws, "ws", torch.uint8)
+    _on_device(Q=Q, ws=ws)
+    check(lib.mcs_block_topk(s, ptr(Q), ptr(means), C, BK, kb, ptr(kv_len), ptr(blocks), ptr(ws), ws.numel(),
+                             stream_ptr()), "mcs_block_topk")
+    return blocks
+
+
+def block_attn(Q, K, V, blocks, C: int, BK: int, R=None, kv_len=None, k_scale=None, v_scale=None, out=None, lse=None,
+               want_lse: bool = False, ws=None, scale=None):
+    """Attention over the key blocks that each block of C query rows lists; returns (out, lse), lse
+    None unless wanted.
+
+    Q [B, H, Nq, d] bf16; K, V [B, Hkv, Nk, d] bf16, or float8_e4m3fn with k_scale and v_scale fp32
+    [B, Hkv, Nk / BK].  blocks: int32 [B, H, ceil(Nq / C), kb] (a list ends at its first negative
+    entry), or None for every block.  kv_len: int32 [B], valid keys of each batch entry.  R: bf16
+    like Q, added to the result.  A row without a key gives R (0 without R) and lse = -inf."""
+    B, H, Nq, d = shape = _heads(Q, "Q")
+    if not isinstance(K, torch.Tensor) or K.dtype not in (torch.bfloat16, E4M3):
+        raise ValueError(f"K must be {torch.bfloat16} or {E4M3}")
+    Hkv, Nk = _heads(K, "K", K.dtype)[1:3]
+    _spec(K, "K", K.dtype, (B, Hkv, Nk, d))
+    _spec(V, "V", K.dtype, (B, Hkv, Nk, d))
+    _kv_heads(H, Hkv)
+    _block_sizes(C, BK)
+    nb = -(-Nk // BK)
+    fp8 = K.dtype == E4M3
+    if fp8:
+        if Nk % BK:
+            raise ValueError(f"an 8-bit cache holds whole blocks: {Nk} rows are no multiple of {BK}")
+        _spec(k_scale, "k_scale", torch.float32, (B, Hkv, nb))
+        _spec(v_scale, "v_scale", torch.float32, (B, Hkv, nb))
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("scales belong to 8-bit K and V")
+    kb = nb
+    if blocks is not None:
+        if not isinstance(blocks, torch.Tensor) or blocks.dim() != 4:
+            raise ValueError("blocks must be a 4-d tensor [B, H, ceil(Nq / C), kb]")
+        kb = blocks.shape[-1]
+        _spec(blocks, "blocks", torch.int32, (B, H, -(-Nq // C), kb))
+        if not 1 <= kb <= nb:
+            raise ValueError(f"blocks must list 1 to {nb} blocks, got {kb}")
+    _length(kv_len, "kv_len", B)
+    if R is not None:
+        _spec(R, "R", torch.bfloat16, shape)
+    if out is None:
+        out = torch.empty_like(Q)
+    _spec(out, "out", torch.bfloat16, shape)
+    if want_lse and lse is None:
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=Q.device)
+    if lse is not None:
+        _spec(lse, "lse", torch.float32, (B, H, Nq))
+    _on_device(Q=Q, K=K, V=V, blocks=blocks, R=R, kv_len=kv_len, k_scale=k_scale, v_scale=v_scale, out=out, lse=lse)
+    _apart(dict(out=out, lse=lse), dict(Q=Q, K=K, V=V, R=R, blocks=blocks))
+    lib = _lib.load()
+    s = _lib.BlockShape(B, H, Hkv, Nq, Nk, d, 0.0 if scale is None else float(scale))
+    if ws is None:
+        n = int(lib.mcs_block_attn_workspace_size(s, C, BK, kb))
+        if n == 0:
+            raise _lib.MCSError(2, "mcs_block_attn_workspace_size: invalid shape")
+        ws = torch.empty(n, dtype=torch.uint8, device=Q.device)
+    _spec(ws, "ws", torch.uint8)
+    _on_device(Q=Q, ws=ws)
+    check(lib.mcs_block_attn(s, ptr(Q), ptr(K), ptr(V), int(fp8), ptr(k_scale), ptr(v_scale), ptr(blocks), C, BK, kb,
+                             ptr(kv_len), ptr(R), ptr(out), ptr(lse), ptr(ws), ws.numel(), stream_ptr()),
+          "mcs_block_attn")
+    return out, lse
+
+
+def cache_write(K, V, K8, V8, k_scale, v_scale, BK: int, start: int = 0, means=None, lens=None):
+    """Write K and V (bf16 [B, H, n, d]) into rows [start, start + n) of an 8-bit store K8, V8
+    (float8_e4m3fn [B, H, capacity, d]) with one scale for each block of BK rows and head (fp32
+    [B, H, capacity / BK]), and each block's mean key into means (fp32 [B, H, capacity / BK, d]) if
+    given.  start and capacity are multiples of BK; a block's scale comes from this call's rows, so an
+    unfinished block is lengthened by writing its rows again.  lens: int32 [B], valid rows of this
+    call; rows behind them stay as they were."""
+    B, H, n, d = _heads(K, "K")
+    _spec(V, "V", torch.bfloat16, (B, H, n, d))
+    _block_sizes(BK=BK)
+    cap = _heads(K8, "K8", E4M3)[2]
+    _spec(K8, "K8", E4M3, (B, H, cap, d))
+    _spec(V8, "V8", E4M3, (B, H, cap, d))
+    if cap % BK or start % BK or start < 0 or start + n > cap:
+        raise ValueError(f"rows [{start}, {start + n}) must lie in the store's {cap}, both multiples of BK = {BK}")
+    _spec(k_scale, "k_scale", torch.float32, (B, H, cap // BK))
+    _spec(v_scale, "v_scale", torch.float32, (B, H, cap // BK))
+    if means is not None:
+        _spec(means, "means", torch.float32, (B, H, cap // BK, d))
+    _length(lens, "lens", B)
+    _on_device(K=K, V=V, K8=K8, V8=V8, k_scale=k_scale, v_scale=v_scale, means=means, lens=lens)
+    check(_lib.load().mcs_cache_write(Shape(B, H, n, d, 0.0), ptr(K), ptr(V), BK, start, cap, ptr(lens), ptr(K8),
+                                      ptr(V8), ptr(k_scale), ptr(v_scale), ptr(means), stream_ptr()), "mcs_cache_write")
+
+
+class KVCache:
+    """Keys and values of one layer in 8 bits, for attention from new frames or tokens to all earlier
+    ones: e4m3 values, one scale per block of BK tokens and head, and each block's mean key, which
+    scores the blocks without reading them.
+
+    append() adds rows (an unfinished last block keeps its bf16 rows beside the store, so that it is
+    quantised anew, with its own scale, whenever it grows); attend() runs attention over every
+    block, or over the kb blocks that block_topk picks for each block of C query rows."""
+
+    def __init__(self, B: int, Hkv: int, capacity: int, d: int, BK: int = 64, device=None):
+        _block_sizes(BK=BK)
+        if capacity < 1 or capacity % BK:
+            raise ValueError(f"capacity must be a positive multiple of BK = {BK}, got {capacity}")
+        dev = "cuda" if device is None else device
+        self.B, self.Hkv, self.capacity, self.d, self.BK, self.length = B, Hkv, capacity, d, BK, 0
+        self.K8, self.V8 = (torch.zeros((B, Hkv, capacity, d), dtype=torch.uint8, device=dev).view(E4M3) for _ in range(2))
+        self.k_scale, self.v_scale = (torch.ones((B, Hkv, capacity // BK), device=dev) for _ in range(2))
+        self.means = torch.zeros((B, Hkv, capacity // BK, d), device=dev)
+        self.kv_len = torch.zeros(B, dtype=torch.int32, device=dev)
+        self._open = None  # bf16 rows of the unfinished last block
+
+    def append(self, K, V):
+        """Add K, V (bf16 [B, Hkv, n, d]) behind the rows held so far."""
+        if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+            raise ValueError("append() keeps its place on the host: a captured one would write the same rows again")
+        n = _heads(K, "K")[2]
+        shape = (self.B, self.Hkv, n, self.d)
+        _spec(K, "K", torch.bfloat16, shape)
+        _spec(V, "V", torch.bfloat16, shape)
+        if self.length + n > self.capacity:
+            raise ValueError(f"{n} more rows do not fit: {self.length} of {self.capacity} are held")
+        tail = self.length % self.BK
+        if tail:
+            K, V = (torch.cat([o, x], 2) for o, x in zip(self._open, (K, V)))
+        cache_write(K, V, self.K8, self.V8, self.k_scale, self.v_scale, self.BK, start=self.length - tail,
+                    means=self.means)
+        self.length += n
+        self.kv_len.fill_(self.length)
+        tail = self.length % self.BK
+        self._open = tuple(x[:, :, x.shape[2] - tail:].clone() for x in (K, V)) if tail else None
+
+    def attend(self, Q, C: int = 128, kb=None, R=None, want_lse: bool = False, scale=None):
+        """(out, lse) of block_attn over the rows held; kb blocks per query block, or all of them."""
+        blocks = None
+        if kb is not None:
+            blocks = block_topk(Q, self.means, C, kb, self.BK, kv_len=self.kv_len)
+        return block_attn(Q, self.K8, self.V8, blocks, C, self.BK, R=R, kv_len=self.kv_len, k_scale=self.k_scale,
+                          v_scale=self.v_scale, want_lse=want_lse, scale=scale)
+
+
 def head_shard(n_heads: int, rank: int, world: int):
     """[lo, hi): the contiguous share of a layer's B*H heads that rank `rank` of `world`
     processes.  Every step of the path (grouping, selection, dense and sparse attention, the

@@ -1,0 +1,290 @@
+// Argument checks, workspace sizes and launches of the block-sparse path (rotary, block means and
+// choice, the 8-bit store, attention over listed blocks).  Part of the library's one translation
+// unit: mcs_api.cu includes it after its own helpers.
+#pragma once
+
+#include "block_attn.cuh"
+
+namespace {
+
+mcs_status check_block_shape(const mcs_block_shape& s) {
+  if (s.B < 1 || s.H < 1 || s.Hkv < 1 || s.Nq < 1 || s.Nk < 1) return MCS_ERR_INVALID_ARG;
+  if (s.d != 64 && s.d != 128) return MCS_ERR_SHAPE;
+  if (s.H % s.Hkv || static_cast<long long>(s.B) * s.H > 65535) return MCS_ERR_SHAPE;
+  // keys and query rows are 32-bit row numbers (TMA coordinates, row counters)
+  if (s.Nq > (1 << 24) || s.Nk > (1 << 24) || static_cast<long long>(s.B) * s.H * s.Nq > 0x7FFFFFFFll ||
+      static_cast<long long>(s.B) * s.Hkv * s.Nk > 0x7FFFFFFFll)
+    return MCS_ERR_SHAPE;
+  return MCS_OK;
+}
+bool block_rows_ok(int BK) { return BK == 32 || BK == 64 || BK == 128; }
+bool query_rows_ok(int C) { return C == 1 || C == 16 || C == 64 || C == 128; }
+
+// Opt-in shared memory of the block-sparse kernels, once per device.
+mcs_status block_device(DeviceInfo** out) {
+  mcs_status e = current_device(out);
+  if (e != MCS_OK) return e;
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (!(*out)->block_attrs_set) {
+    const int topk = kTopkMaxBlocks * 8;
+    if (cudaFuncSetAttribute(block_topk_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, topk) != cudaSuccess ||
+        cudaFuncSetAttribute(block_topk_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, topk) != cudaSuccess)
+      return MCS_ERR_CUDA;
+    (*out)->block_attrs_set = true;
+  }
+  return MCS_OK;
+}
+
+template <int HD, int NORM>
+void launch_rotary(const RotaryParams& p, bool halves, cudaStream_t st) {
+  const unsigned grid = static_cast<unsigned>(p.B) * static_cast<unsigned>(p.tiles);
+  if (halves) rotary_kernel<HD, NORM, true><<<grid, kRotThreads, 0, st>>>(p);
+  else rotary_kernel<HD, NORM, false><<<grid, kRotThreads, 0, st>>>(p);
+}
+template <int HD>
+void launch_rotary(const RotaryParams& p, int norm, bool halves, cudaStream_t st) {
+  if (norm == kNormNone) launch_rotary<HD, kNormNone>(p, halves, st);
+  else if (norm == kNormHead) launch_rotary<HD, kNormHead>(p, halves, st);
+  else launch_rotary<HD, kNormToken>(p, halves, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+mcs_status mcs_rotary(const mcs_rotary_args* a, const void* q, const void* k, const void* v, const void* pos,
+                      const void* q_weight, const void* k_weight, void* Q, void* K, void* V, void* stream) {
+  if (!a) return MCS_ERR_INVALID_ARG;
+  if (a->B < 1 || a->N < 1 || a->H < 1 || a->Hkv < 1) return MCS_ERR_INVALID_ARG;
+  if (a->d != 64 && a->d != 128) return MCS_ERR_SHAPE;
+  if (a->N > (1 << 24) || static_cast<long long>(a->B) * a->N > 0x7FFFFFFFll || a->H > 65535 || a->Hkv > 65535)
+    return MCS_ERR_SHAPE;
+  if (a->axes < 1 || a->axes > kRotMaxAxes || a->norm < kNormNone || a->norm > kNormToken ||
+      (a->pairs != 0 && a->pairs != 1) || !(a->theta > 0) || !(a->theta < 1e300) || !(a->eps >= 0.f) ||
+      !(a->eps < 3e38f))
+    return MCS_ERR_INVALID_ARG;
+  int sum = 0;
+  for (int i = 0; i < a->axes; ++i) {
+    if (a->axis_dim[i] < 2 || a->axis_dim[i] % 2) return MCS_ERR_SHAPE;
+    sum += a->axis_dim[i];
+    if (sum > a->d) return MCS_ERR_SHAPE;
+  }
+  if (a->pairs == 1 && sum % 16) return MCS_ERR_SHAPE;  // the halves meet on an 8-element boundary
+  if (!q || !Q || !pos || !k != !K || !v != !V) return MCS_ERR_INVALID_ARG;
+  const void* src[3] = {q, k, v};
+  void* dst[3] = {Q, K, V};
+  for (int s = 0; s < 3; ++s) {
+    if (!src[s]) continue;
+    if (!aligned16(src[s]) || !aligned16(dst[s])) return MCS_ERR_DTYPE_ALIGN;
+    for (int i = 0; i < 3; ++i) {
+      if (a->stride[s][i] < 0) return MCS_ERR_INVALID_ARG;
+      if (a->stride[s][i] % 8) return MCS_ERR_DTYPE_ALIGN;
+    }
+  }
+  if ((q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight)) || (reinterpret_cast<uintptr_t>(pos) & 3u))
+    return MCS_ERR_DTYPE_ALIGN;
+  DeviceInfo* di = nullptr;
+  mcs_status e = block_device(&di);
+  if (e != MCS_OK) return e;
+  RotaryParams p{};
+  for (int s = 0; s < 3; ++s) {
+    p.x[s] = static_cast<const __nv_bfloat16*>(src[s]);
+    p.y[s] = static_cast<__nv_bfloat16*>(dst[s]);
+    p.sb[s] = a->stride[s][0];
+    p.sn[s] = a->stride[s][1];
+    p.sh[s] = a->stride[s][2];
+    p.heads[s] = s == 0 ? a->H : a->Hkv;
+  }
+  p.w[0] = q_weight;
+  p.w[1] = k_weight;
+  p.pos = pos;
+  constexpr double kTwoPi = 6.283185307179586476925;
+  int at = 0;
+  for (int i = 0; i < a->axes; ++i)
+    for (int j = 0; j < a->axis_dim[i] / 2; ++j, ++at) {
+      p.turns[at] = std::pow(a->theta, -2.0 * j / a->axis_dim[i]) / kTwoPi;
+      p.axis[at] = static_cast<unsigned char>(i);
+    }
+  p.B = a->B;
+  p.N = a->N;
+  p.A = a->axes;
+  p.half = at;
+  p.pos_float = a->pos_is_float != 0;
+  p.pos_batch = a->pos_per_batch != 0;
+  p.w_bf16 = a->weight_is_bf16 != 0;
+  p.eps = a->eps;
+  // 16 tokens a CTA (4 KB of consecutive output per head at d = 128) unless that leaves SMs idle
+  p.T = kRotMaxTokens;
+  while (p.T > 1 && static_cast<long long>(a->B) * ((a->N + p.T - 1) / p.T) < 2ll * di->sms) p.T /= 2;
+  p.tiles = (a->N + p.T - 1) / p.T;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (a->d == 64) launch_rotary<64>(p, a->norm, a->pairs == 1, st);
+  else launch_rotary<128>(p, a->norm, a->pairs == 1, st);
+  return launch_status();
+}
+
+mcs_status mcs_block_means(mcs_shape s, const void* X, int BK, const int32_t* len, float* means, void* stream) {
+  mcs_status e = check_shape(s);
+  if (e != MCS_OK) return e;
+  if (!block_rows_ok(BK)) return MCS_ERR_SHAPE;
+  if (!X || !means) return MCS_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(means) || (reinterpret_cast<uintptr_t>(len) & 3u)) return MCS_ERR_DTYPE_ALIGN;
+  DeviceInfo* di = nullptr;
+  if ((e = block_device(&di)) != MCS_OK) return e;
+  MeansParams p{};
+  p.X = static_cast<const __nv_bfloat16*>(X);
+  p.len = len;
+  p.means = means;
+  p.H = s.H;
+  p.N = s.N;
+  p.BK = BK;
+  p.nb = (s.N + BK - 1) / BK;
+  p.blocks = static_cast<long long>(s.B) * s.H * p.nb;
+  const unsigned grid = static_cast<unsigned>((p.blocks + kMeansThreads / 32 - 1) / (kMeansThreads / 32));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (s.d == 64) block_means_kernel<64><<<grid, kMeansThreads, 0, st>>>(p);
+  else block_means_kernel<128><<<grid, kMeansThreads, 0, st>>>(p);
+  return launch_status();
+}
+
+size_t mcs_block_topk_workspace_size(mcs_block_shape s, int C, int BK) {
+  if (check_block_shape(s) != MCS_OK || !query_rows_ok(C) || !block_rows_ok(BK) || (s.Nk + BK - 1) / BK > kTopkMaxBlocks)
+    return 0;
+  return 256;
+}
+
+mcs_status mcs_block_topk(mcs_block_shape s, const void* Q, const float* means, int C, int BK, int kb,
+                          const int32_t* kv_len, int32_t* blocks, void* ws, size_t ws_bytes, void* stream) {
+  mcs_status e = check_block_shape(s);
+  if (e != MCS_OK) return e;
+  if (!query_rows_ok(C) || !block_rows_ok(BK) || (s.Nk + BK - 1) / BK > kTopkMaxBlocks) return MCS_ERR_SHAPE;
+  const int nb = (s.Nk + BK - 1) / BK;
+  if (kb < 1 || kb > nb || !Q || !means || !blocks) return MCS_ERR_INVALID_ARG;
+  if (!aligned16(Q) || !aligned16(means) || (reinterpret_cast<uintptr_t>(blocks) & 3u) ||
+      (reinterpret_cast<uintptr_t>(kv_len) & 3u))
+    return MCS_ERR_DTYPE_ALIGN;
+  if (!ws || ws_bytes < mcs_block_topk_workspace_size(s, C, BK)) return MCS_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(ws) & 255u) return MCS_ERR_DTYPE_ALIGN;
+  DeviceInfo* di = nullptr;
+  if ((e = block_device(&di)) != MCS_OK) return e;
+  TopkParams p{};
+  p.Q = static_cast<const __nv_bfloat16*>(Q);
+  p.means = means;
+  p.len = kv_len;
+  p.blocks = blocks;
+  p.H = s.H;
+  p.Hkv = s.Hkv;
+  p.Nq = s.Nq;
+  p.Nk = s.Nk;
+  p.GQ = (s.Nq + C - 1) / C;
+  p.C = C;
+  p.BK = BK;
+  p.nb = nb;
+  p.kb = kb;
+  const dim3 grid(p.GQ, s.B * s.H);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (s.d == 64) block_topk_kernel<64><<<grid, kTopkThreads, static_cast<size_t>(nb) * 8, st>>>(p);
+  else block_topk_kernel<128><<<grid, kTopkThreads, static_cast<size_t>(nb) * 8, st>>>(p);
+  return launch_status();
+}
+
+mcs_status mcs_cache_write(mcs_shape s, const void* K, const void* V, int BK, int start, int capacity,
+                           const int32_t* len, void* K8, void* V8, float* k_scale, float* v_scale, float* means,
+                           void* stream) {
+  mcs_status e = check_shape(s);
+  if (e != MCS_OK) return e;
+  if (!block_rows_ok(BK) || capacity < 1 || capacity % BK || capacity > (1 << 24) ||
+      static_cast<long long>(s.B) * s.H * capacity > 0x7FFFFFFFll)
+    return MCS_ERR_SHAPE;
+  if (start < 0 || start % BK || static_cast<long long>(start) + s.N > capacity) return MCS_ERR_INVALID_ARG;
+  if (!K || !V || !K8 || !V8 || !k_scale || !v_scale) return MCS_ERR_INVALID_ARG;
+  if (!aligned16(K) || !aligned16(V) || !aligned16(K8) || !aligned16(V8) || !aligned16(k_scale) || !aligned16(v_scale) ||
+      (means && !aligned16(means)) || (reinterpret_cast<uintptr_t>(len) & 3u))
+    return MCS_ERR_DTYPE_ALIGN;
+  DeviceInfo* di = nullptr;
+  if ((e = block_device(&di)) != MCS_OK) return e;
+  CacheWriteParams p{};
+  p.X[0] = static_cast<const __nv_bfloat16*>(K);
+  p.X[1] = static_cast<const __nv_bfloat16*>(V);
+  p.Y[0] = static_cast<uint8_t*>(K8);
+  p.Y[1] = static_cast<uint8_t*>(V8);
+  p.scale[0] = k_scale;
+  p.scale[1] = v_scale;
+  p.means = means;
+  p.len = len;
+  p.H = s.H;
+  p.n = s.N;
+  p.cap = capacity;
+  p.start = start;
+  p.BK = BK;
+  p.nb = (s.N + BK - 1) / BK;
+  const dim3 grid(p.nb, s.B * s.H, 2);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (s.d == 64) cache_write_kernel<64><<<grid, kCacheThreads, 0, st>>>(p);
+  else cache_write_kernel<128><<<grid, kCacheThreads, 0, st>>>(p);
+  return launch_status();
+}
+
+size_t mcs_block_attn_workspace_size(mcs_block_shape s, int C, int BK, int kb) {
+  if (check_block_shape(s) != MCS_OK || !query_rows_ok(C) || !block_rows_ok(BK) || kb < 1 || kb > (s.Nk + BK - 1) / BK)
+    return 0;
+  return 256;
+}
+
+mcs_status mcs_block_attn(mcs_block_shape s, const void* Q, const void* K, const void* V, int kv_format,
+                          const float* k_scale, const float* v_scale, const int32_t* blocks, int C, int BK, int kb,
+                          const int32_t* kv_len, const void* R, void* out, float* lse, void* ws, size_t ws_bytes,
+                          void* stream) {
+  mcs_status e = check_block_shape(s);
+  if (e != MCS_OK) return e;
+  if (!query_rows_ok(C) || !block_rows_ok(BK)) return MCS_ERR_SHAPE;
+  const int nb = (s.Nk + BK - 1) / BK;
+  if (kb < 1 || kb > nb || (!blocks && kb != nb) || (kv_format != 0 && kv_format != 1)) return MCS_ERR_INVALID_ARG;
+  if (kv_format == 1 && s.Nk % BK) return MCS_ERR_SHAPE;
+  if (!Q || !K || !V || !out || (kv_format == 1) != (k_scale != nullptr) || (kv_format == 1) != (v_scale != nullptr))
+    return MCS_ERR_INVALID_ARG;
+  if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(out) || (R && !aligned16(R)) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(blocks) & 3u) ||
+      (reinterpret_cast<uintptr_t>(kv_len) & 3u) || (reinterpret_cast<uintptr_t>(k_scale) & 3u) ||
+      (reinterpret_cast<uintptr_t>(v_scale) & 3u))
+    return MCS_ERR_DTYPE_ALIGN;
+  if (!ws || ws_bytes < mcs_block_attn_workspace_size(s, C, BK, kb)) return MCS_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(ws) & 255u) return MCS_ERR_DTYPE_ALIGN;
+  DeviceInfo* di = nullptr;
+  if ((e = block_device(&di)) != MCS_OK) return e;
+  BlockAttnParams p{};
+  p.Q = static_cast<const __nv_bfloat16*>(Q);
+  p.K = K;
+  p.V = V;
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.blocks = blocks;
+  p.len = kv_len;
+  p.R = static_cast<const __nv_bfloat16*>(R);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.B = s.B;
+  p.H = s.H;
+  p.Hkv = s.Hkv;
+  p.Nq = s.Nq;
+  p.Nk = s.Nk;
+  p.C = C;
+  p.BK = BK;
+  p.nb = nb;
+  p.GQ = (s.Nq + C - 1) / C;
+  p.kb = kb;
+  p.scale_log2 = (s.scale > 0.f ? s.scale : 1.0f / std::sqrt(static_cast<float>(s.d))) * kLog2e;
+  const long long rows = static_cast<long long>(s.B) * s.H * s.Nq;
+  const unsigned grid = static_cast<unsigned>((rows + kSimpleWarps - 1) / kSimpleWarps);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (s.d == 64) {
+    if (kv_format) block_attn_simple_kernel<64, true><<<grid, kSimpleWarps * 32, 0, st>>>(p);
+    else block_attn_simple_kernel<64, false><<<grid, kSimpleWarps * 32, 0, st>>>(p);
+  } else {
+    if (kv_format) block_attn_simple_kernel<128, true><<<grid, kSimpleWarps * 32, 0, st>>>(p);
+    else block_attn_simple_kernel<128, false><<<grid, kSimpleWarps * 32, 0, st>>>(p);
+  }
+  return launch_status();
+}
+
+}  // extern "C"

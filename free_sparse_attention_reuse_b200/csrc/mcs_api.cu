@@ -26,6 +26,7 @@ struct DeviceInfo {
   bool supported = false;
   int sms = 0;
   bool attrs_set = false;
+  bool block_attrs_set = false;
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mu;
@@ -832,3 +833,5 @@ extern "C" mcs_status mcs_select_noalloc(mcs_shape s, const void* Q, const void*
   return select_impl(s, Q, K, perm, C, k, lse, idx, reinterpret_cast<char*>(scratch), w,
                      static_cast<cudaStream_t>(stream));
 }
+
+#include "block_api.cuh"

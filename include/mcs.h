@@ -215,6 +215,90 @@ size_t mcs_kmeans_workspace_size(mcs_shape s, int C);
 mcs_status mcs_group_kmeans(mcs_shape s, const void* Q, int C, int iters, int32_t* perm, void* ws, size_t ws_bytes,
                             void* stream);
 
+/* ---- Block-sparse attention without an anchor step: from a layer's projections to attention over key
+ * blocks that a cheap score picks anew at every step, with the keys and values of earlier frames kept in
+ * 8 bits.  Additions of this library (P4, section 무엇인가, describes block scores from mean-pooled queries
+ * and keys as the common practice; the pages give no kernel for them).  Unlike the calls above these take
+ * different numbers of query and key rows, fewer key/value heads than query heads, any lengths, and
+ * lengths per batch entry.  Forward only, like everything here.
+ *
+ *   Q, O, R : bf16 [B, H, Nq, d]             K, V : bf16 or e4m3 [B, Hkv, Nk, d], Hkv divides H
+ *   means   : fp32 [B, Hkv, nb, d]           nb = ceil(Nk / BK) key blocks of BK = 32, 64 or 128 keys
+ *   blocks  : int32 [B, H, GQ, kb]           GQ = ceil(Nq / C) query blocks of C = 1, 16, 64 or 128 rows
+ *   kv_len  : int32 [B], nullable            valid keys of each batch entry (NULL: Nk everywhere)
+ *
+ * Query head h reads key/value head h / (H / Hkv).  A kv_len entry outside [0, Nk] is reported as
+ * MCS_ERR_BAD_INDEX and clamped.  Keys behind kv_len are never read into a result, whatever they hold
+ * (NaN and infinities included).  int32 and fp32 vectors indexed by batch or block need 4-byte alignment
+ * only; workspaces 256. */
+typedef struct {
+  int B, H, Hkv, Nq, Nk, d;
+  float scale; /* softmax scale; <= 0 means 1/sqrt(d) */
+} mcs_block_shape;
+
+/* Arguments of mcs_rotary that are not tensors. */
+typedef struct {
+  int B, N, H, Hkv, d;
+  int axes;                /* number of position axes, 1 to 4                                         */
+  int axis_dim[4];         /* even number of elements that each axis turns; their sum is at most d     */
+  double theta;            /* base of the frequencies                                                 */
+  float eps;               /* of the norm                                                             */
+  int pairs;               /* 0: a pair is elements 2i, 2i+1; 1: i and i + sum/2 (sum % 16 == 0)       */
+  int norm;                /* 0: none, 1: over a head's d elements, 2: over all heads of a token       */
+  int pos_is_float;        /* pos is fp32 (else int32)                                                */
+  int pos_per_batch;       /* pos is [B, N, axes] (else [N, axes])                                     */
+  int weight_is_bf16;      /* norm weights are bf16 (else fp32)                                       */
+  long long stride[3][3];  /* elements between batch entries, tokens and heads of q, k and v; each a
+                              multiple of 8 (the d elements of a row are consecutive)                 */
+} mcs_rotary_args;
+
+/* Projections to attention-ready tensors: q [B, N, H, d], k and v [B, N, Hkv, d] (bf16 views with the
+ * given strides, 16-byte aligned) to Q [B, H, N, d], K and V [B, Hkv, N, d] (contiguous).
+ *   q and k rows:  x <- x rsqrt(mean(x^2) + eps) w  (norm 1: mean over the row, weight [d]; norm 2: over the
+ *                  token's heads, weight [heads, d]; w = 1 where the weight is NULL),
+ *                  then pair i turns by pos[axis(i)] * theta^(-2 j / axis_dim), j its place in its axis's
+ *                  section: (x1 cos - x2 sin, x1 sin + x2 cos).  Elements behind the axes' sum do not turn.
+ *   v is copied.  k and K, v and V may be NULL together.  Outputs must not alias inputs.
+ * All in fp32 (angles in fp64), rounded once. */
+mcs_status mcs_rotary(const mcs_rotary_args* a, const void* q, const void* k, const void* v, const void* pos,
+                      const void* q_weight, const void* k_weight, void* Q, void* K, void* V, void* stream);
+
+/* means[b,h,j,:] = mean of the valid rows of block j of X [B, H, N, d] (s.N rows, len valid ones; zero for
+ * a block without one), BK = 32, 64 or 128.  Sums in fp64, result fp32. */
+mcs_status mcs_block_means(mcs_shape s, const void* X, int BK, const int32_t* len, float* means, void* stream);
+
+/* The kb key blocks of largest score for every query block: score(g, j) = mean of g's query rows (rounded to
+ * fp32) . means[j], in fp64; among blocks that hold a valid key, ties to the lower block, NaN below every
+ * number.  blocks[b,h,g,:] ascends; -1 behind the chosen where fewer than kb blocks are valid.
+ * 1 <= kb <= nb <= 24576; MCS_ERR_SHAPE beyond. */
+size_t mcs_block_topk_workspace_size(mcs_block_shape s, int C, int BK);
+mcs_status mcs_block_topk(mcs_block_shape s, const void* Q, const float* means, int C, int BK, int kb,
+                          const int32_t* kv_len, int32_t* blocks, void* ws, size_t ws_bytes, void* stream);
+
+/* Keys and values into an 8-bit store: rows [start, start + s.N) of K8, V8 [B, H, capacity, d] (e4m3), block by
+ * block: scale = max(amax / 448, 2^-100) (1 for a block of zeros), value = e4m3(x / scale) to nearest even,
+ * saturating; k_scale and v_scale are fp32 [B, H, capacity / BK].  amax runs over the finite values of the
+ * block's rows of this call; NaN is stored as NaN, an infinity as the largest value.  means (nullable, fp32
+ * [B, H, capacity / BK, d]) gets the mean of each block's keys before rounding, as mcs_block_means.
+ * start and capacity are multiples of BK (a block is written whole: to lengthen an unfinished one, write its
+ * rows again).  len (nullable, int32 [B]): valid rows of this call for each batch entry; rows behind them,
+ * and blocks without a valid row, stay as they were. */
+mcs_status mcs_cache_write(mcs_shape s, const void* K, const void* V, int BK, int start, int capacity,
+                           const int32_t* len, void* K8, void* V8, float* k_scale, float* v_scale, float* means,
+                           void* stream);
+
+/* out[i] = sum_j softmax_j(scale q_i . k_j) v_j + R[i] over the valid keys j of the blocks that i's query block
+ * lists (a list ends at its first negative entry; an entry >= nb is reported as MCS_ERR_BAD_INDEX and
+ * skipped; a block listed twice counts twice); blocks = NULL: every block, kb = nb.
+ * lse[b,h,i] (nullable, fp32) = log sum_j exp(scale q_i . k_j).  A row without a key: out = R (0 without R),
+ * lse = -inf.  kv_format 0: K, V bf16, no scales; 1: e4m3 with k_scale, v_scale fp32 [B, Hkv, nb] (positive
+ * and finite, as mcs_cache_write makes them), Nk a multiple of BK.  R nullable; out must not alias an input. */
+size_t mcs_block_attn_workspace_size(mcs_block_shape s, int C, int BK, int kb);
+mcs_status mcs_block_attn(mcs_block_shape s, const void* Q, const void* K, const void* V, int kv_format,
+                          const float* k_scale, const float* v_scale, const int32_t* blocks, int C, int BK, int kb,
+                          const int32_t* kv_len, const void* R, void* out, float* lse, void* ws, size_t ws_bytes,
+                          void* stream);
+
 /* Synchronise `stream`, then read and clear the device status word of the current device:
  * MCS_OK, MCS_ERR_BAD_INDEX, MCS_ERR_TIMEOUT, or MCS_ERR_CUDA if the stream reports an error.
  * There is one word per device, shared by the library's kernels on every stream: with calls
