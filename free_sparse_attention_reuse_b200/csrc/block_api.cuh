@@ -21,6 +21,16 @@ bool block_rows_ok(int BK) { return BK == 32 || BK == 64 || BK == 128; }
 bool query_rows_ok(int C) { return C == 1 || C == 16 || C == 64 || C == 128; }
 
 // Opt-in shared memory of the block-sparse kernels, once per device.
+template <int HD, bool KV8, bool PAIR>
+bool block_attn_attrs() {
+  // the kernel moves registers between its warpgroups and counts on 128 a thread at launch: a build
+  // with another count would wait for registers that never come, so it is refused here
+  cudaFuncAttributes fa{};
+  return cudaFuncSetAttribute(block_attn_kernel<HD, KV8, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              BlockSmem<HD>::BYTES) == cudaSuccess &&
+         cudaFuncGetAttributes(&fa, block_attn_kernel<HD, KV8, PAIR>) == cudaSuccess &&
+         static_cast<long long>(fa.numRegs) * kAttnThreads == 65536;
+}
 mcs_status block_device(DeviceInfo** out) {
   mcs_status e = current_device(out);
   if (e != MCS_OK) return e;
@@ -28,11 +38,80 @@ mcs_status block_device(DeviceInfo** out) {
   if (!(*out)->block_attrs_set) {
     const int topk = kTopkMaxBlocks * 8;
     if (cudaFuncSetAttribute(block_topk_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, topk) != cudaSuccess ||
-        cudaFuncSetAttribute(block_topk_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, topk) != cudaSuccess)
+        cudaFuncSetAttribute(block_topk_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, topk) != cudaSuccess ||
+        !block_attn_attrs<64, false, false>() || !block_attn_attrs<64, false, true>() ||
+        !block_attn_attrs<64, true, false>() || !block_attn_attrs<64, true, true>() ||
+        !block_attn_attrs<128, false, false>() || !block_attn_attrs<128, false, true>() ||
+        !block_attn_attrs<128, true, false>() || !block_attn_attrs<128, true, true>())
       return MCS_ERR_CUDA;
     (*out)->block_attrs_set = true;
   }
   return MCS_OK;
+}
+
+// How a call of mcs_block_attn runs; a function of its sizes alone, so that the workspace's size and the
+// launch agree.  Without lists every query head of a key/value head attends to the same keys: their
+// rows, which lie one behind the other, count as one head's.
+struct BlockPlan {
+  bool tensor;       // the tcgen05 kernel (else one warp per row)
+  bool pair;         // lists of 64 rows: two to a tile
+  int H, Nq, C, GQ;  // as the kernel sees them
+  int tiles, splits;
+  size_t part, total;  // workspace: bytes of the parts' results, and all
+};
+constexpr int kPlanSms = 148;
+
+BlockPlan plan_block_attn(const mcs_block_shape& s, int C, int BK, int kb, bool listed) {
+  BlockPlan q{};
+  q.H = listed ? s.H : s.Hkv;
+  q.Nq = listed ? s.Nq : s.Nq * (s.H / s.Hkv);
+  q.C = C;
+  q.tensor = listed ? C >= 64 : q.Nq > 16;
+  q.pair = q.tensor && listed && C == 64;
+  q.GQ = (q.Nq + C - 1) / C;
+  q.tiles = (q.Nq + kTile - 1) / kTile;
+  q.splits = 1;
+  if (q.tensor) {
+    if (!q.pair) q.GQ = q.tiles;
+    // Few tiles: the keys of a tile are split over several CTAs.  The cost of a choice, in stages of
+    // 128 keys: waves times (the part's stages and about three of start and end), and six for the
+    // join's launch.
+    const long long units = static_cast<long long>(s.B) * q.H * q.tiles;
+    const int T = static_cast<int>((static_cast<long long>(kb) * BK + kTile - 1) / kTile);
+    long long best = -1;
+    for (int n = 1; n <= 32 && (n == 1 || T / n >= 4); ++n) {
+      const long long cost = (units * n + kPlanSms - 1) / kPlanSms * ((T + n - 1) / n + 3) + (n > 1 ? 6 : 0);
+      if (best < 0 || cost < best) best = cost, q.splits = n;
+    }
+  }
+  const size_t rows = static_cast<size_t>(s.B) * s.H * s.Nq;
+  if (q.splits > 1) q.part = round_up(rows * q.splits * s.d * 4, 256);
+  q.total = q.part + (q.splits > 1 ? round_up(rows * q.splits * 4, 256) : 256);
+  return q;
+}
+
+template <int HD, bool KV8, bool PAIR>
+mcs_status run_block_attn(const BlockAttnParams& p, cudaStream_t st, int sms) {
+  alignas(64) CUtensorMap tmQ, tmK, tmV;
+  if (!make_row_map(&tmQ, p.Q, static_cast<uint64_t>(p.B) * p.H * p.Nq, HD, kTile)) return MCS_ERR_CUDA;
+  if (KV8) {
+    tmK = tmV = tmQ;  // not used: 8-bit rows are loaded to registers
+  } else {
+    const uint64_t rows = static_cast<uint64_t>(p.B) * p.Hkv * p.Nk;
+    if (!make_row_map(&tmK, p.K, rows, HD, p.BK) || !make_row_map(&tmV, p.V, rows, HD, p.BK)) return MCS_ERR_CUDA;
+  }
+  block_attn_kernel<HD, KV8, PAIR><<<std::min(p.num_units, sms), kAttnThreads, BlockSmem<HD>::BYTES, st>>>(tmQ, tmK, tmV, p);
+  if (p.splits > 1) {
+    const long long rows = static_cast<long long>(p.B) * p.H * p.Nq;
+    constexpr int per = 256 / (HD / 4);
+    block_join_kernel<HD><<<static_cast<unsigned>((rows + per - 1) / per), 256, 0, st>>>(p);
+  }
+  return launch_status();
+}
+template <int HD>
+mcs_status run_block_attn(const BlockAttnParams& p, bool kv8, bool pair, cudaStream_t st, int sms) {
+  if (kv8) return pair ? run_block_attn<HD, true, true>(p, st, sms) : run_block_attn<HD, true, false>(p, st, sms);
+  return pair ? run_block_attn<HD, false, true>(p, st, sms) : run_block_attn<HD, false, false>(p, st, sms);
 }
 
 template <int HD, int NORM>
@@ -228,7 +307,8 @@ mcs_status mcs_cache_write(mcs_shape s, const void* K, const void* V, int BK, in
 size_t mcs_block_attn_workspace_size(mcs_block_shape s, int C, int BK, int kb) {
   if (check_block_shape(s) != MCS_OK || !query_rows_ok(C) || !block_rows_ok(BK) || kb < 1 || kb > (s.Nk + BK - 1) / BK)
     return 0;
-  return 256;
+  const size_t n = plan_block_attn(s, C, BK, kb, true).total;
+  return kb < (s.Nk + BK - 1) / BK ? n : std::max(n, plan_block_attn(s, C, BK, kb, false).total);
 }
 
 mcs_status mcs_block_attn(mcs_block_shape s, const void* Q, const void* K, const void* V, int kv_format,
@@ -263,20 +343,31 @@ mcs_status mcs_block_attn(mcs_block_shape s, const void* Q, const void* K, const
   p.R = static_cast<const __nv_bfloat16*>(R);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
+  const BlockPlan plan = plan_block_attn(s, C, BK, kb, blocks != nullptr);
+  p.part = static_cast<float*>(ws);
+  p.plse = reinterpret_cast<float*>(static_cast<char*>(ws) + plan.part);
   p.B = s.B;
-  p.H = s.H;
+  p.H = plan.H;
   p.Hkv = s.Hkv;
-  p.Nq = s.Nq;
+  p.Nq = plan.Nq;
   p.Nk = s.Nk;
-  p.C = C;
+  p.C = plan.C;
   p.BK = BK;
   p.nb = nb;
-  p.GQ = (s.Nq + C - 1) / C;
+  p.GQ = plan.GQ;
   p.kb = kb;
+  p.tiles = plan.tiles;
+  p.splits = plan.splits;
+  p.num_units = static_cast<int>(static_cast<long long>(s.B) * plan.H * plan.tiles * plan.splits);
   p.scale_log2 = (s.scale > 0.f ? s.scale : 1.0f / std::sqrt(static_cast<float>(s.d))) * kLog2e;
+  p.wait_ns = g_attn_wait_ns.load();
+  p.hold = g_attn_hold.load();
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (plan.tensor)
+    return s.d == 64 ? run_block_attn<64>(p, kv_format != 0, plan.pair, st, di->sms)
+                     : run_block_attn<128>(p, kv_format != 0, plan.pair, st, di->sms);
   const long long rows = static_cast<long long>(s.B) * s.H * s.Nq;
   const unsigned grid = static_cast<unsigned>((rows + kSimpleWarps - 1) / kSimpleWarps);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (s.d == 64) {
     if (kv_format) block_attn_simple_kernel<64, true><<<grid, kSimpleWarps * 32, 0, st>>>(p);
     else block_attn_simple_kernel<64, false><<<grid, kSimpleWarps * 32, 0, st>>>(p);

@@ -20,8 +20,13 @@ struct BlockAttnParams {
   const __nv_bfloat16* R;   // [B, H, Nq, d], nullable
   __nv_bfloat16* out;       // [B, H, Nq, d]
   float* lse;               // [B, H, Nq], nullable
+  float* part;              // [splits, B * H * Nq, d]: normalised partial results (splits > 1)
+  float* plse;              // [splits, B * H * Nq]: their log-sum-exps in base 2
   int B, H, Hkv, Nq, Nk, C, BK, nb, GQ, kb;
-  float scale_log2;         // scale * log2(e)
+  int tiles, splits, num_units;  // query tiles of a head; parts of a tile's keys; B * H * tiles * splits
+  float scale_log2;              // scale * log2(e)
+  unsigned long long wait_ns;    // bound on any single wait of this launch (nanoseconds)
+  const uint32_t* hold;          // test hook (normally NULL): wait for *hold != 0 before any MMA
 };
 
 constexpr int kSimpleWarps = 4;
@@ -123,6 +128,848 @@ __global__ void __launch_bounds__(kSimpleWarps * 32) block_attn_simple_kernel(co
     p.out[at] = __float2bfloat16(v);
   }
   if (p.lse != nullptr && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+// ---------------------------------------------------------------------------------- tensor-core form
+// A warp's walk over the usable entries of one list: block numbers within the store that hold a valid
+// key, up to the first negative entry.  32 entries at a time, the next 32 fetched ahead.
+struct ListWalk {
+  const int32_t* list;  // nullable: every block in turn
+  int kb, nb, BK, len;
+  int w0, id, nid, left;  // first entry of the window, this lane's entry, the next window's, entries to go
+  uint32_t mask;          // usable entries of the window not taken yet
+  bool end;               // a negative entry lies in the window (or the list is over)
+
+  __device__ __forceinline__ int fetch(int w) const {
+    const int i = w + static_cast<int>(lane_id());
+    return i >= kb ? -1 : list != nullptr ? list[i] : i;
+  }
+  __device__ __forceinline__ void window(bool report) {
+    id = nid;
+    const uint32_t neg = __ballot_sync(0xffffffffu, id < 0);
+    const int upto = neg ? __ffs(neg) - 1 : 32;
+    const bool in = static_cast<int>(lane_id()) < upto;
+    if (report && in && id >= nb) raise_status(kStatusBadIndex);
+    mask = __ballot_sync(0xffffffffu, in && id < nb && static_cast<long long>(id) * BK < len);
+    end = neg != 0;
+    if (!end) nid = fetch(w0 + 32);
+  }
+  // Usable entries of the whole list.
+  __device__ __forceinline__ int count(bool report) {
+    int n = 0;
+    w0 = 0;
+    nid = fetch(0);
+    for (;;) {
+      window(report);
+      n += __popc(mask);
+      if (end) return n;
+      w0 += 32;
+    }
+  }
+  // Start again at usable entry `lo`, to take `n` of them.
+  __device__ __forceinline__ void start(int lo, int n) {
+    left = n;
+    mask = 0;
+    if (n <= 0) return;
+    w0 = 0;
+    nid = fetch(0);
+    for (;;) {
+      window(false);
+      const int c = __popc(mask);
+      if (lo < c) break;
+      lo -= c;
+      if (end) break;
+      w0 += 32;
+    }
+    for (; lo > 0; --lo) mask &= mask - 1;
+  }
+  // The next block, or -1.
+  __device__ __forceinline__ int next() {
+    if (left <= 0) return -1;
+    --left;
+    while (mask == 0) {
+      if (end) return -1;
+      w0 += 32;
+      window(false);
+    }
+    const int l = __ffs(mask) - 1;
+    mask &= mask - 1;
+    return __shfl_sync(0xffffffffu, id, l);
+  }
+};
+
+// Valid keys, and scales, of a stage's four runs of 32 keys (each within one block).
+struct StageInfo {
+  int valid[4];
+  float ks[4], vs[4];
+};
+
+template <int HD>
+struct BlockSmem {
+  static constexpr uint32_t TILE_BYTES = kTile * HD * 2;
+  static constexpr int KST = HD == 128 ? 3 : 6;
+  static constexpr int VST = HD == 128 ? 3 : 6;
+  static constexpr uint32_t Q_OFF = 0;
+  static constexpr uint32_t K_OFF = Q_OFF + TILE_BYTES;
+  static constexpr uint32_t V_OFF = K_OFF + KST * TILE_BYTES;
+  static constexpr uint32_t XCH_OFF = V_OFF + VST * TILE_BYTES;  // 2 streams x 128 rows x (m, l)
+  static constexpr uint32_t INFO_OFF = XCH_OFF + 2 * kTile * 8;  // StageInfo[KST]
+  static constexpr uint32_t UNIT_OFF = INFO_OFF + KST * sizeof(StageInfo);  // stages of both streams, 4 units
+  static constexpr uint32_t BAR_OFF = UNIT_OFF + 4 * 8;
+  // q_full, q_empty, k_full[KST], k_empty[KST], v_full[VST], v_empty[VST]; per stream s_full, p_full,
+  // pv_done, p_half, pvlo_done; o_empty, drain, vfix, pair[4], u_full[4]
+  static constexpr int NBAR = 2 + 2 * KST + 2 * VST + 10 + 3 + 4 + 4;
+  static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
+  static constexpr uint32_t BYTES = MISC_OFF + 16;
+  static_assert(BAR_OFF % 8 == 0 && INFO_OFF % 16 == 0, "shared memory alignment");
+  static_assert(BYTES <= 232448, "shared memory budget");
+};
+
+// Registers a thread: softmax (two warpgroups), producers, MMA; the 8-bit form's producers hold two
+// tiles' worth of loads each.
+template <bool KV8>
+struct BlockRegs {
+  static constexpr uint32_t SOFTMAX = KV8 ? 184 : 192, PRODUCER = KV8 ? 96 : 80, MMA = 48;
+  static_assert(2 * 128 * SOFTMAX + 128 * PRODUCER + 128 * MMA <= 512 * 128, "more registers than the launch has");
+};
+
+// 16 e4m3 values to bf16 (exact: 4 significant bits, exponents in range).
+__device__ __forceinline__ void e4m3_to_bf16(const uint4& u, uint32_t* w) {
+  const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __nv_fp8x2_storage_t x = static_cast<__nv_fp8x2_storage_t>(in[i >> 1] >> ((i & 1) * 16));
+    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(x, __NV_E4M3)));
+    w[i] = pack_bf16x2(f.x, f.y);
+  }
+}
+
+// The pipeline of attn_kernel (two softmax streams per tile of 128 query rows, S and O in TMEM, P over
+// S) with the keys of listed blocks in stages of 128: 128 / BK blocks a stage, a TMA box each, or,
+// from an 8-bit store, loaded to registers, widened to bf16 and stored by the four producer warps.
+//   PAIR = false  both streams work on the tile's 128 rows, alternate stages; merged at the end.
+//   PAIR = true   lists of 64 rows: stream A takes rows 0-63 with their list, stream B rows 64-127
+//                 with theirs.  The MMAs compute all 128 rows either way; each stream's two idle
+//                 warps leave its other half alone, so no exponential is spent on it, and the
+//                 active warps lie on all four sub-partitions.
+// A unit with no usable entry has one stage of 128 masked keys, so that every unit takes the same path.
+template <int HD, bool KV8, bool PAIR>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    block_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const BlockAttnParams p) {
+  using L = BlockSmem<HD>;
+  using RG = BlockRegs<KV8>;
+  constexpr int KST = L::KST, VST = L::VST;
+  constexpr uint32_t HALF = kTile * 128;
+  constexpr uint32_t IDESC_QK = idesc_bf16(128, kTile, false, false);
+  constexpr uint32_t IDESC_PV = idesc_bf16(128, HD, false, true);
+  constexpr uint32_t ACTIVE = PAIR ? 64 : 128;  // softmax threads of a stream
+  constexpr uint32_t LAUNCH_REGS = 65536 / kAttnThreads;
+
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t base = smem_u32(smem_raw);
+  if (base & 1023u) {  // uniform across the CTA: nothing has started yet
+    if (threadIdx.x == 0) raise_status(kStatusBadShape);
+    return;
+  }
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw + L::BAR_OFF);
+  uint64_t* q_full = bars + 0;
+  uint64_t* q_empty = bars + 1;
+  uint64_t* k_full = bars + 2;
+  uint64_t* k_empty = k_full + KST;
+  uint64_t* v_full = k_empty + KST;
+  uint64_t* v_empty = v_full + VST;
+  uint64_t* s_full = v_empty + VST;  // [2], per stream, as the next four
+  uint64_t* p_full = s_full + 2;
+  uint64_t* pv_done = p_full + 2;
+  uint64_t* p_half = pv_done + 2;
+  uint64_t* pvlo_done = p_half + 2;
+  uint64_t* o_empty = pvlo_done + 2;
+  uint64_t* drain = o_empty + 1;
+  uint64_t* vfix = drain + 1;    // V stage whose last rows are cleared before it is handed on
+  uint64_t* pair = vfix + 1;     // [4], one per row group (its two warps)
+  uint64_t* u_full = pair + 4;   // [4], unit counts published
+  StageInfo* sInfo = reinterpret_cast<StageInfo*>(smem_raw + L::INFO_OFF);
+  int2* sUnit = reinterpret_cast<int2*>(smem_raw + L::UNIT_OFF);
+  float2* sXch = reinterpret_cast<float2*>(smem_raw + L::XCH_OFF);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + L::MISC_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_raw + L::MISC_OFF + 4);
+
+  const uint32_t sQ = base + L::Q_OFF, sK = base + L::K_OFF, sV = base + L::V_OFF;
+  const int warp = warp_id(), lane = lane_id();
+  const uint64_t wl = p.wait_ns;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int s = 0; s < KST; ++s) {
+      mbar_init(k_full + s, KV8 ? 128 : 1);
+      mbar_init(k_empty + s, ACTIVE);
+    }
+    for (int s = 0; s < VST; ++s) {
+      mbar_init(v_full + s, KV8 ? 128 : 1);
+      mbar_init(v_empty + s, 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(s_full + x, 1);
+      mbar_init(p_full + x, ACTIVE);
+      mbar_init(pv_done + x, 1);
+      mbar_init(p_half + x, ACTIVE);
+      mbar_init(pvlo_done + x, 1);
+    }
+    mbar_init(o_empty, 2 * ACTIVE);
+    mbar_init(drain, 1);
+    mbar_init(vfix, 1);
+    for (int g = 0; g < 4; ++g) mbar_init(pair + g, 64);
+    for (int g = 0; g < 4; ++g) mbar_init(u_full + g, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // The stages of a unit alternate between the streams while both have one; the longer stream's rest
+  // follows.  tn = (stages of A, stages of B).
+  auto stage_pos = [](int2 tn, int x, int i) {  // place of stream x's stage i in the unit
+    const int m = min(tn.x, tn.y);
+    return i < m ? 2 * i + x : m + i;
+  };
+
+  if (warp >= 8 && warp < 12) {
+    // ------------------------------------------------------------------ producer
+    regs_to<RG::PRODUCER, LAUNCH_REGS>();
+    const int pw = warp - 8;
+    if (KV8 || pw == 0) {
+      const int BPS = kTile / p.BK;  // blocks of a stage
+      uint32_t kv_it = 0, u_it = 0, q_issued = 0, k_issued = 0, v_issued = 0, n_fix = 0;
+      bool okp = true;
+      for (int unit = blockIdx.x; unit < p.num_units && okp; unit += gridDim.x, ++u_it) {
+        const int sp = unit % p.splits, tu = unit / p.splits;
+        const int bh = tu / p.tiles, ut = tu - bh * p.tiles;
+        const int b = bh / p.H, bkv = b * p.Hkv + (bh - b * p.H) / (p.H / p.Hkv);
+        ListWalk wk[PAIR ? 2 : 1];
+        int tn[2] = {0, 0};
+#pragma unroll
+        for (int x = 0; x < (PAIR ? 2 : 1); ++x) {
+          const int g = PAIR ? 2 * ut + x : ut;
+          wk[x].kb = p.kb;
+          wk[x].nb = p.nb;
+          wk[x].BK = p.BK;
+          wk[x].len = valid_rows(p.len, b, p.Nk);
+          if (g >= p.GQ) {  // an odd last list: stream B has no rows here
+            wk[x].start(0, 0);
+            continue;
+          }
+          wk[x].list = p.blocks != nullptr ? p.blocks + (static_cast<size_t>(bh) * p.GQ + g) * p.kb : nullptr;
+          const int n = p.blocks != nullptr ? wk[x].count(pw == 0) : min(p.nb, (wk[x].len + p.BK - 1) / p.BK);
+          const int lo = static_cast<int>(static_cast<long long>(n) * sp / p.splits);
+          const int hi = static_cast<int>(static_cast<long long>(n) * (sp + 1) / p.splits);
+          wk[x].start(lo, hi - lo);
+          tn[x] = max(1, (hi - lo + BPS - 1) / BPS);
+        }
+        const int T = tn[0] + tn[1];
+        if (!PAIR) {
+          tn[1] = T / 2;
+          tn[0] = T - tn[1];
+        }
+        const int2 tn2 = make_int2(tn[0], tn[1]);
+        const int both = 2 * min(tn[0], tn[1]), longer = tn[0] >= tn[1] ? 0 : 1;
+        if (pw == 0) {
+          // (the slot's unit is four back: the MMAs of the unit before this one are issued, so the
+          // epilogue of the one two before that has read its counts)
+          if (!mbar_wait_warp(q_empty, (u_it & 1) ^ 1, abort_flag, wl)) { okp = false; break; }
+          if (lane == 0) {
+            sUnit[u_it & 3] = tn2;
+            mbar_arrive(u_full + (u_it & 3));
+            mbar_arrive_expect_tx(q_full, L::TILE_BYTES);
+#pragma unroll
+            for (int h = 0; h < HD / 64; ++h)
+              tma_load_2d(sQ + h * HALF, &tmQ, h * 64, bh * p.Nq + ut * kTile, q_full);
+          }
+          ++q_issued;
+          __syncwarp();
+        }
+        if constexpr (!KV8) {
+          for (int t = 0; t < T; ++t, ++kv_it) {
+            const uint32_t ks = kv_it % KST, vs = kv_it % VST;
+            ListWalk& w = wk[PAIR ? (t < both ? t & 1 : longer) : 0];
+            int blk[4];  // the stage's blocks (-1: none)
+            int short_rows = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              blk[i] = i < BPS ? w.next() : -1;
+              if (blk[i] >= 0 && w.len - blk[i] * p.BK < p.BK) short_rows = 1;
+            }
+            // run r (32 keys) lies in block r * 32 / BK of the stage
+            int mine = blk[0];
+#pragma unroll
+            for (int i = 1; i < 4; ++i)
+              if ((lane & 3) * 32 / p.BK == i) mine = blk[i];
+            const int valid = mine < 0 ? 0 : min(32, max(0, w.len - mine * p.BK - ((lane & 3) * 32) % p.BK));
+            int loads = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) loads += blk[i] >= 0 ? 1 : 0;
+            const uint32_t bytes = static_cast<uint32_t>(loads * p.BK) * HD * 2;
+            if (!mbar_wait_warp(k_empty + ks, ((kv_it / KST) & 1) ^ 1, abort_flag, wl)) { okp = false; break; }
+            if (lane < 4) sInfo[ks].valid[lane] = valid;
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive_expect_tx(k_full + ks, bytes);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (blk[i] >= 0)
+#pragma unroll
+                  for (int h = 0; h < HD / 64; ++h)
+                    tma_load_2d(sK + ks * L::TILE_BYTES + h * HALF + i * p.BK * 128, &tmK, h * 64,
+                                bkv * p.Nk + blk[i] * p.BK, k_full + ks);
+            }
+            ++k_issued;
+            __syncwarp();
+            if (!mbar_wait_warp(v_empty + vs, ((kv_it / VST) & 1) ^ 1, abort_flag, wl)) { okp = false; break; }
+            const uint32_t dV = sV + vs * L::TILE_BYTES;
+            // masked keys weigh 0, but 0 times whatever lies in their V rows need not be 0: rows of no
+            // block are cleared beside the copies, rows behind the last valid one after theirs
+            const bool gaps = loads < BPS;
+            if (gaps) {
+              for (int r = loads * p.BK + lane; r < kTile; r += 32)
+#pragma unroll
+                for (int c = 0; c < HD / 8; ++c)
+                  asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dV + sw128_offset(r, c, kTile)), "r"(0u)
+                               : "memory");
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            uint64_t* land = short_rows ? vfix : v_full + vs;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(land, bytes);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (blk[i] >= 0)
+#pragma unroll
+                  for (int h = 0; h < HD / 64; ++h)
+                    tma_load_2d(dV + h * HALF + i * p.BK * 128, &tmV, h * 64, bkv * p.Nk + blk[i] * p.BK, land);
+            }
+            __syncwarp();
+            if (short_rows) {
+              mbar_drain(vfix, n_fix & 1);
+              ++n_fix;
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const int vr = __shfl_sync(0xffffffffu, valid, r);
+                if (lane >= vr)
+#pragma unroll
+                  for (int c = 0; c < HD / 8; ++c)
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dV + sw128_offset(r * 32 + lane, c, kTile)),
+                                 "r"(0u)
+                                 : "memory");
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(v_full + vs);
+            }
+            ++v_issued;
+            __syncwarp();
+          }
+        } else {
+          // ---- 8-bit rows: this warp's run of 32 keys of every stage
+          constexpr int LPR = HD / 16, RPI = 32 / LPR, NIT = 32 / RPI;
+          const int sub = lane / LPR, c = lane % LPR;
+          uint4 bk[NIT], bv[NIT];
+          float fks = 1.f, fvs = 1.f;
+          int valid = 0;
+          auto fetch = [&](int t) {
+            ListWalk& w = wk[PAIR ? (t < both ? t & 1 : longer) : 0];
+            int mine = -1;
+            for (int i = 0; i < BPS; ++i) {
+              const int x = w.next();
+              if (pw * 32 / p.BK == i) mine = x;
+            }
+            const int row0 = mine * p.BK + (pw * 32) % p.BK;
+            valid = mine < 0 ? 0 : min(32, max(0, w.len - row0));
+            fks = fvs = 1.f;
+            if (mine >= 0) {
+              fks = p.ks[static_cast<size_t>(bkv) * p.nb + mine];
+              fvs = p.vs[static_cast<size_t>(bkv) * p.nb + mine];
+            }
+            const size_t at = (static_cast<size_t>(bkv) * p.Nk + (mine < 0 ? 0 : row0)) * HD + c * 16;
+#pragma unroll
+            for (int it = 0; it < NIT; ++it) {
+              const int r = it * RPI + sub;
+              const bool in = r < valid;
+              bk[it] = in ? *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.K) + at + r * HD) : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int it = 0; it < NIT; ++it) {
+              const int r = it * RPI + sub;
+              const bool in = r < valid;
+              bv[it] = in ? *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.V) + at + r * HD) : make_uint4(0u, 0u, 0u, 0u);
+            }
+          };
+          // a lane's 16 values are two 16-byte chunks; every other lane stores its second one first,
+          // so that a store's eight lanes of a row group hit all eight bank groups
+          auto put = [&](uint32_t tile, const uint4* buf) {
+#pragma unroll
+            for (int it = 0; it < NIT; ++it) {
+              uint32_t w[8];
+              e4m3_to_bf16(buf[it], w);
+              const int r = pw * 32 + it * RPI + sub;
+              const bool swap = HD == 128 ? (c & 4) != 0 : (sub & 1) != 0;
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const bool second = (k == 1) != swap;
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(tile + sw128_offset(r, 2 * c + (second ? 1 : 0), kTile)),
+                             "r"(second ? w[4] : w[0]), "r"(second ? w[5] : w[1]), "r"(second ? w[6] : w[2]),
+                             "r"(second ? w[7] : w[3])
+                             : "memory");
+              }
+            }
+            fence_proxy_async_smem();
+          };
+          fetch(0);
+          for (int t = 0; t < T; ++t, ++kv_it) {
+            const uint32_t ks = kv_it % KST, vs = kv_it % VST;
+            if (!mbar_wait_warp(k_empty + ks, ((kv_it / KST) & 1) ^ 1, abort_flag, wl)) { okp = false; break; }
+            if (lane == 0) {
+              sInfo[ks].valid[pw] = valid;
+              sInfo[ks].ks[pw] = fks;
+              sInfo[ks].vs[pw] = fvs;
+            }
+            put(sK + ks * L::TILE_BYTES, bk);
+            mbar_arrive(k_full + ks);
+            if (!mbar_wait_warp(v_empty + vs, ((kv_it / VST) & 1) ^ 1, abort_flag, wl)) { okp = false; break; }
+            put(sV + vs * L::TILE_BYTES, bv);
+            mbar_arrive(v_full + vs);
+            if (t + 1 < T) fetch(t + 1);
+          }
+        }
+      }
+      if (pw == 0 && !okp) {
+        // after an abort, the TMA loads already issued land before the CTA releases its shared memory
+        // (on a normal exit every load has been consumed)
+        if (q_issued > 0) mbar_drain(q_full, (q_issued - 1) & 1);
+        if constexpr (!KV8) {
+          for (uint32_t s = 0; s < static_cast<uint32_t>(KST) && s < k_issued; ++s) {
+            const uint32_t last = k_issued - 1 - ((k_issued - 1 + KST - s) % KST);
+            mbar_drain(k_full + s, (last / KST) & 1);
+          }
+          for (uint32_t s = 0; s < static_cast<uint32_t>(VST) && s < v_issued; ++s) {
+            const uint32_t last = v_issued - 1 - ((v_issued - 1 + VST - s) % VST);
+            mbar_drain(v_full + s, (last / VST) & 1);
+          }
+        }
+      }
+    }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------------ MMA issuer
+    regs_to<RG::MMA, LAUNCH_REGS>();
+    if (warp == 12) {
+      const uint64_t dQ = desc_sw128(sQ, 16, 1024);
+      const uint64_t dK0 = desc_sw128(sK, 16, 1024);
+      const uint64_t dV0 = desc_sw128(sV, HALF, 1024);
+      constexpr uint64_t kSlotStep = L::TILE_BYTES >> 4;
+      uint32_t kv_base = 0, u_it = 0;
+      uint32_t sc0 = 0, sc1 = 0;  // PVs issued per stream (barrier phases)
+      bool ok = true;
+      if (p.hold != nullptr) {
+        if (lane == 0) {
+          const uint64_t t0 = globaltimer_ns();
+          while (ld_acquire_gpu_u32(p.hold) == 0u) {
+            if (globaltimer_ns() - t0 > wl) {
+              raise_status(kStatusTimeout);
+              *abort_flag = 1;
+              ok = false;
+              break;
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      }
+      for (int unit = blockIdx.x; unit < p.num_units && ok; unit += gridDim.x, ++u_it) {
+        ok = mbar_wait_warp(u_full + (u_it & 3), (u_it >> 2) & 1, abort_flag, wl);
+        if (!ok) break;
+        const int2 tn = sUnit[u_it & 3];
+        const int T = tn.x + tn.y, both = 2 * min(tn.x, tn.y), longer = tn.x >= tn.y ? 0 : 1;
+        ok = mbar_wait_warp(q_full, u_it & 1, abort_flag, wl);
+        if (!ok) break;
+        auto qk_mmas = [&](int t, int x) {  // S_x of the stage at place t
+          const uint32_t ks = (kv_base + t) % KST;
+          const uint64_t dK = dK0 + ks * kSlotStep;
+          const uint32_t dS = tmem + kTmS + x * kTile;
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            const uint64_t koff = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+            mma_bf16_ss_warp(dS, dQ + koff, dK + koff, IDESC_QK, kk > 0 ? 1u : 0u);
+          }
+          mma_commit_warp(s_full + x);
+          if (t == T - 1) mma_commit_warp(q_empty);
+        };
+        auto wait_k = [&](int t) -> bool {
+          const uint32_t it = kv_base + t;
+          return mbar_wait_warp(k_full + it % KST, (it / KST) & 1, abort_flag, wl);
+        };
+        // the first stage of each stream: places 0 and 1 (place 1 of a lone stream A waits its turn)
+        ok = wait_k(0) && (both == 0 || wait_k(1));
+        if (!ok) break;
+        qk_mmas(0, 0);
+        if (both > 0) qk_mmas(1, 1);
+        int n0 = 0, n1 = 0;  // stages of each stream done in this unit
+        for (int t = 0; t < T && ok; ++t) {
+          const int x = t < both ? t & 1 : longer;
+          const int mine = x ? n1 : n0;  // which stage of its stream
+          const bool next = mine + 1 < (x ? tn.y : tn.x);
+          const int tnext = next ? stage_pos(tn, x, mine + 1) : 0;
+          const uint32_t it = kv_base + t, vs = it % VST;
+          ok = mbar_wait_warp(p_half + x, (x ? sc1 : sc0) & 1, abort_flag, wl) &&
+               mbar_wait_warp(v_full + vs, (it / VST) & 1, abort_flag, wl) &&
+               (t != 0 || mbar_wait_warp(o_empty, (u_it & 1) ^ 1, abort_flag, wl));
+          if (!ok) break;
+          tc_fence_after();  // P_x was written by tcgen05.st of the softmax
+          const uint64_t dV = dV0 + vs * kSlotStep;
+          const uint32_t tO = tmem + kTmO + x * HD, tP = tmem + kTmS + x * kTile;
+          const bool first = mine == 0;  // overwrites O_x
+#pragma unroll
+          for (int kk = 0; kk < 2 * kPSplit; ++kk)
+            mma_bf16_ts_warp(tO, tP + kk * 8, dV + kk * (2048 >> 4), IDESC_PV, (!first || kk > 0) ? 1u : 0u);
+          mma_commit_warp(pvlo_done + x);
+          ok = mbar_wait_warp(p_full + x, (x ? sc1 : sc0) & 1, abort_flag, wl) && (!next || wait_k(tnext));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 2 * kPSplit; kk < kTile / 16; ++kk)
+            mma_bf16_ts_warp(tO, tP + kk * 8, dV + kk * (2048 >> 4), IDESC_PV, 1u);
+          mma_commit_warp(pv_done + x);
+          mma_commit_warp(v_empty + vs);
+          if (x) ++sc1, ++n1;
+          else ++sc0, ++n0;
+          if (next) qk_mmas(tnext, x);
+        }
+        kv_base += T;
+      }
+      mma_commit_warp(drain);
+      mbar_drain(drain, 0);
+    }  // warps 13-15 only complete the warpgroup
+  } else {
+    // ------------------------------------------------------------------ softmax + epilogue
+    regs_to<RG::SOFTMAX, LAUNCH_REGS>();
+    const int rg = warp & 3, x = warp >> 2;  // row group, stream
+    if (!PAIR || (rg >> 1) == x) {
+      const int row = rg * 32 + lane;  // tile row == TMEM lane
+      const uint32_t lane_base = static_cast<uint32_t>(rg * 32) << 16;
+      const uint32_t tS = tmem + lane_base + kTmS + x * kTile;
+      const uint32_t tOx = tmem + lane_base + kTmO + x * HD;
+      const float sl2 = p.scale_log2;
+      uint32_t sc = 0, kv_base = 0, u_it = 0;
+      bool ok = true;
+      for (int unit = blockIdx.x; unit < p.num_units && ok; unit += gridDim.x, ++u_it) {
+        const int sp = unit % p.splits, tu = unit / p.splits;
+        const int bh = tu / p.tiles, ut = tu - bh * p.tiles;
+        const int qrow = ut * kTile + row;
+        const bool live = qrow < p.Nq;
+        if (!mbar_wait_warp(u_full + (u_it & 3), (u_it >> 2) & 1, abort_flag, wl)) { ok = false; break; }
+        const int2 tn = sUnit[u_it & 3];
+        const int Tx = x ? tn.y : tn.x;
+        float m_used = -INFINITY, l_part = 0.f;  // -inf: no key of weight yet
+        float m_pend = -INFINITY;  // a raise of the reference decided by the stream's previous stage
+        for (int i = 0; i < Tx; ++i, ++sc) {
+          if (!mbar_wait_warp(s_full + x, sc & 1, abort_flag, wl)) { ok = false; break; }
+          const uint32_t slot = (kv_base + stage_pos(tn, x, i)) % KST;
+          const int4 v4 = *reinterpret_cast<const int4*>(sInfo[slot].valid);
+          const int vq[4] = {v4.x, v4.y, v4.z, v4.w};
+          float kq[4] = {sl2, sl2, sl2, sl2}, vsq[4] = {1.f, 1.f, 1.f, 1.f};
+          if (KV8) {
+            const float4 a = *reinterpret_cast<const float4*>(sInfo[slot].ks);
+            const float4 b = *reinterpret_cast<const float4*>(sInfo[slot].vs);
+            kq[0] *= a.x, kq[1] *= a.y, kq[2] *= a.z, kq[3] *= a.w;
+            vsq[0] = b.x, vsq[1] = b.y, vsq[2] = b.z, vsq[3] = b.w;
+          }
+          // the QK^T that wrote S has read its K slot: hand the slot back to the producer
+          mbar_arrive(k_empty + slot);
+          tc_fence_after();
+          auto rescale_o = [&](float alpha) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < HD; c0 += 32) {
+              uint32_t o[32];
+              tmem_ld32(tOx + c0, o);
+              tmem_ld_wait_regs(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(tOx + c0, o);
+            }
+          };
+          auto signal_half = [&]() {
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(p_half + x);
+          };
+          // P = exp2(S * scale - m) of one run of 32 keys, times its V scale, in bf16 pairs, and its
+          // sums over the even and the odd keys
+          auto chunk_exps = [&](const uint32_t* sr, int v, float k, float vs, float m, uint32_t* pk, float2& cs) {
+            cs = make_float2(0.f, 0.f);
+            const float2 k2 = make_float2(k, k), nm2 = make_float2(-m, -m), v2 = make_float2(vs, vs);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const float2 xv =
+                  __ffma2_rn(make_float2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), k2, nm2);
+              float2 e = make_float2(fast_exp2(xv.x), fast_exp2(xv.y));
+              if (v < 32) {
+                e.x = 2 * c < v ? e.x : 0.f;
+                e.y = 2 * c + 1 < v ? e.y : 0.f;
+              }
+              cs = __fadd2_rn(cs, e);
+              if (KV8) e = __fmul2_rn(e, v2);
+              pk[c] = pack_bf16x2(e.x, e.y);
+            }
+          };
+          uint32_t sr[128];
+          tmem_ld32(tS, sr);
+          tmem_ld32(tS + 32, sr + 32);
+          tmem_ld32(tS + 64, sr + 64);
+          tmem_ld32(tS + 96, sr + 96);
+          tmem_ld_wait_regs(sr);
+          reg_fence32(sr + 32);
+          reg_fence32(sr + 64);
+          reg_fence32(sr + 96);
+          // Rows without a reference yet (the first stage, or every key so far masked or at -inf; O_x
+          // and l are 0 then) take the stage's exact maximum.
+          if (i == 0 || __any_sync(0xffffffffu, m_used == -INFINITY)) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float a = -INFINITY, b = -INFINITY;
+              if (vq[q] >= 32) {
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                  a = fmaxf(a, __uint_as_float(sr[32 * q + c]));
+                  b = fmaxf(b, __uint_as_float(sr[32 * q + c + 1]));
+                }
+              } else {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) a = fmaxf(a, c < vq[q] ? __uint_as_float(sr[32 * q + c]) : -INFINITY);
+              }
+              mx = fmaxf(mx, fmaxf(a, b) * kq[q]);
+            }
+            if (m_used == -INFINITY) m_used = mx;
+          }
+          // A stage whose P summed past 2^16 raised the reference for this one, applied once the
+          // stream's previous PV has completed so that O_x and l follow.
+          if (__any_sync(0xffffffffu, m_pend > m_used)) {
+            if (!mbar_wait_warp(pv_done + x, (sc - 1) & 1, abort_flag, wl)) { ok = false; break; }
+            tc_fence_after();
+            const float alpha = m_pend > m_used ? fast_exp2(m_used - m_pend) : 1.f;
+            rescale_o(alpha);
+            l_part *= alpha;
+            m_used = fmaxf(m_used, m_pend);
+          }
+          float2 rs = make_float2(0.f, 0.f);
+          // known complete: the stream's previous PV (o_prev), also this stage's first part (o_lo)
+          bool o_prev = false, o_lo = false;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t pk[16];
+            float2 cs;
+            chunk_exps(sr + 32 * q, vq[q], kq[q], vsq[q], m_used == -INFINITY ? 0.f : m_used, pk, cs);
+            const bool big = !(cs.x + cs.y <= 4294967296.f);  // 2^32, or inf / NaN
+            if (__any_sync(0xffffffffu, big)) {
+              // rare: raise this row's reference to the run's largest logit by whole octaves (so that
+              // rescaling bf16 P is exact), rescale what is behind it, and redo the run
+              const float mz = m_used == -INFINITY ? 0.f : m_used;
+              float xm = -INFINITY;
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (c < vq[q]) xm = fmaxf(xm, fmaf(__uint_as_float(sr[32 * q + c]), kq[q], -mz));
+              const bool raise = big && xm > 0.f;
+              const float xr = raise ? fminf(ceilf(xm), 65536.f) : 0.f;
+              const int n = static_cast<int>(xr);
+              const float alpha = n >= 127 ? 0.f : __int_as_float((127 - n) << 23);  // 2^-n
+              if (q >= kPSplit && !o_lo) {
+                if (!mbar_wait_warp(pvlo_done + x, sc & 1, abort_flag, wl)) { ok = false; break; }
+                tc_fence_after();
+                o_lo = o_prev = true;
+              } else if (!o_prev) {
+                if (!mbar_wait_warp(pv_done + x, (sc - 1) & 1, abort_flag, wl)) { ok = false; break; }
+                tc_fence_after();
+                o_prev = true;
+              }
+              tmem_st_wait();
+              rescale_o(alpha);
+              l_part *= alpha;
+              rs.x *= alpha;
+              rs.y *= alpha;
+#pragma unroll 1
+              for (int q2 = q >= kPSplit ? kPSplit : 0; q2 < q; ++q2) {
+                uint32_t pv[16];
+                tmem_ld16(tS + 16 * q2, pv);
+                tmem_ld_wait_regs16(pv);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&pv[e]));
+                  pv[e] = pack_bf16x2(f.x * alpha, f.y * alpha);
+                }
+                tmem_st16(tS + 16 * q2, pv);
+              }
+              tmem_st_wait();
+              if (raise) m_used = mz + xr;
+              chunk_exps(sr + 32 * q, vq[q], kq[q], vsq[q], m_used == -INFINITY ? 0.f : m_used, pk, cs);
+            }
+            rs = __fadd2_rn(rs, cs);
+            tmem_st16(tS + 16 * q, pk);
+            if (q == kPSplit - 1) signal_half();
+          }
+          if (!ok) break;
+          const float st = rs.x + rs.y;
+          m_pend = st > 65536.f ? m_used + __log2f(st) : -INFINITY;
+          l_part += st;
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(p_full + x);
+        }
+        if (!ok) break;
+        kv_base += tn.x + tn.y;
+        const size_t orow = static_cast<size_t>(bh) * p.Nq + qrow;
+        const size_t prow = static_cast<size_t>(sp) * p.B * p.H * p.Nq + orow;  // of a split's partial result
+        if (Tx > 0) {
+          // this stream's last PV of the unit
+          if (!mbar_wait_warp(pv_done + x, (sc - 1) & 1, abort_flag, wl)) { ok = false; break; }
+          tc_fence_after();
+        }
+        // 8 output columns from column c on: R is added, or the partial result goes to the workspace
+        auto store8 = [&](int c, float* v) {
+          if (p.splits > 1) {
+            float4* d = reinterpret_cast<float4*>(p.part + prow * HD + c);
+            d[0] = make_float4(v[0], v[1], v[2], v[3]);
+            d[1] = make_float4(v[4], v[5], v[6], v[7]);
+            return;
+          }
+          *reinterpret_cast<uint4*>(p.out + orow * HD + c) = pack8(v);
+        };
+        const bool add = live && p.R != nullptr && p.splits == 1;
+        float m_all = m_used, l_sum = l_part;
+        if constexpr (PAIR) {
+          const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
+#pragma unroll 1
+          for (int c0 = 0; c0 < HD; c0 += 64) {
+            uint4 extra[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              extra[e] = add ? *reinterpret_cast<const uint4*>(p.R + orow * HD + c0 + 8 * e) : make_uint4(0u, 0u, 0u, 0u);
+            uint32_t o[64];
+            tmem_ld64_wait(tOx + c0, o);
+            if (live) {
+#pragma unroll
+              for (int c = 0; c < 64; c += 8) {
+                float v[8], r[8];
+                unpack8(extra[c / 8], r);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = fmaf(__uint_as_float(o[c + e]), inv, r[e]);
+                store8(c0 + c, v);
+              }
+            }
+          }
+        } else {
+          constexpr int NV = HD / 16;  // uint4 (8 bf16) per half row
+          const int cx = x * (HD / 2);
+          uint4 extra[NV];
+#pragma unroll
+          for (int e = 0; e < NV; ++e)
+            extra[e] = add ? *reinterpret_cast<const uint4*>(p.R + orow * HD + cx + 8 * e) : make_uint4(0u, 0u, 0u, 0u);
+          const bool has_b = tn.y > 0;
+          sXch[x * kTile + row] = make_float2(m_used, l_part);
+          tc_fence_before();
+          mbar_arrive(pair + rg);
+          if (!mbar_wait_warp(pair + rg, 0, abort_flag, wl)) { ok = false; break; }
+          tc_fence_after();
+          const float2 xa = sXch[row], xb = sXch[kTile + row];
+          mbar_arrive(pair + rg);
+          if (!mbar_wait_warp(pair + rg, 1, abort_flag, wl)) { ok = false; break; }
+          m_all = fmaxf(xa.x, xb.x);
+          const float mz = m_all == -INFINITY ? 0.f : m_all;
+          const float wA = fast_exp2(xa.x - mz);
+          const float wB = has_b ? fast_exp2(xb.x - mz) : 0.f;
+          l_sum = xa.y * wA + xb.y * wB;
+          const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
+          const float cA = wA * inv, cB = wB * inv;
+          const uint32_t tOA = tmem + lane_base + kTmO + cx, tOB = tOA + HD;
+          uint32_t oab[HD];  // [0, HD/2): O_A; [HD/2, HD): O_B
+          if constexpr (HD == 128) tmem_ld32x4_wait(tOA, tOA + 32, tOB, tOB + 32, oab);
+          else tmem_ld32x2_wait(tOA, tOB, oab);
+          if (live) {
+#pragma unroll
+            for (int c = 0; c < HD / 2; c += 8) {
+              float v[8], r[8];
+              unpack8(extra[c / 8], r);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                // O_B holds no product of this unit when stream B had no stage: leave it out
+                const float ob = has_b ? __uint_as_float(oab[HD / 2 + c + e]) * cB : 0.f;
+                v[e] = fmaf(__uint_as_float(oab[c + e]), cA, ob) + r[e];
+              }
+              store8(cx + c, v);
+            }
+          }
+        }
+        if (live && (PAIR || x == 0)) {
+          const float l2 = l_sum == 0.f ? -INFINITY : m_all + __log2f(l_sum);
+          if (p.splits > 1) p.plse[prow] = l2;
+          else if (p.lse != nullptr) p.lse[orow] = l2 * 0.69314718055994531f;
+        }
+        tc_fence_before();
+        mbar_arrive(o_empty);
+      }
+      // (after an abort) no load or store of this warp is still in flight when TMEM is released
+      tmem_ld_wait();
+      tmem_st_wait();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------------- splits joined
+// out = sum_s 2^(l_s - l) o_s (+ R), l = log2 sum_s 2^l_s over the parts of a row's keys; HD / 4 lanes a row.
+template <int HD>
+__global__ void __launch_bounds__(256) block_join_kernel(const BlockAttnParams p) {
+  constexpr int LPR = HD / 4, RPB = 256 / LPR;
+  const long long rows = static_cast<long long>(p.B) * p.H * p.Nq;
+  const long long row = static_cast<long long>(blockIdx.x) * RPB + threadIdx.x / LPR;
+  const int c = (threadIdx.x % LPR) * 4;
+  if (row >= rows) return;
+  float m = -INFINITY;
+  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, p.plse[s * rows + row]);
+  const float mz = m == -INFINITY ? 0.f : m;
+  float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < p.splits; ++s) {
+    const float w = exp2f(p.plse[s * rows + row] - mz);
+    const float4 v = *reinterpret_cast<const float4*>(p.part + (s * rows + row) * HD + c);
+    l += w;
+    o[0] = fmaf(w, v.x, o[0]);
+    o[1] = fmaf(w, v.y, o[1]);
+    o[2] = fmaf(w, v.z, o[2]);
+    o[3] = fmaf(w, v.w, o[3]);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  float r[4] = {0.f, 0.f, 0.f, 0.f};
+  if (p.R != nullptr) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p.R + row * HD + c);
+    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+    r[0] = a.x, r[1] = a.y, r[2] = b.x, r[3] = b.y;
+  }
+  uint2 w;
+  w.x = pack_bf16x2(fmaf(o[0], inv, r[0]), fmaf(o[1], inv, r[1]));
+  w.y = pack_bf16x2(fmaf(o[2], inv, r[2]), fmaf(o[3], inv, r[3]));
+  *reinterpret_cast<uint2*>(p.out + row * HD + c) = w;
+  if (p.lse != nullptr && c == 0) p.lse[row] = l == 0.f ? -INFINITY : (mz + log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace mcs
