@@ -345,14 +345,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // ------------------------------------------------------------------ producer
     regs_to<RG::PRODUCER, LAUNCH_REGS>();
     const int pw = warp - 8;
-    if (KV8 || pw == 0) {
+    if (KV8 || pw < 2) {
       const int BPS = kTile / p.BK;  // blocks of a stage
-      uint32_t kv_it = 0, u_it = 0, q_issued = 0, k_issued = 0, v_issued = 0, n_fix = 0;
+      const int bk_log = 31 - __clz(p.BK);
+      uint32_t kv_it = 0, u_it = 0, q_issued = 0, issued = 0, n_fix = 0;
       bool okp = true;
       for (int unit = blockIdx.x; unit < p.num_units && okp; unit += gridDim.x, ++u_it) {
         const int sp = unit % p.splits, tu = unit / p.splits;
         const int bh = tu / p.tiles, ut = tu - bh * p.tiles;
         const int b = bh / p.H, bkv = b * p.Hkv + (bh - b * p.H) / (p.H / p.Hkv);
+        const int len = valid_rows(p.len, b, p.Nk);
         ListWalk wk[PAIR ? 2 : 1];
         int tn[2] = {0, 0};
 #pragma unroll
@@ -361,13 +363,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           wk[x].kb = p.kb;
           wk[x].nb = p.nb;
           wk[x].BK = p.BK;
-          wk[x].len = valid_rows(p.len, b, p.Nk);
+          wk[x].len = len;
           if (g >= p.GQ) {  // an odd last list: stream B has no rows here
             wk[x].start(0, 0);
             continue;
           }
           wk[x].list = p.blocks != nullptr ? p.blocks + (static_cast<size_t>(bh) * p.GQ + g) * p.kb : nullptr;
-          const int n = p.blocks != nullptr ? wk[x].count(pw == 0) : min(p.nb, (wk[x].len + p.BK - 1) / p.BK);
+          const int n = p.blocks != nullptr ? wk[x].count(pw == 0) : min(p.nb, (len + p.BK - 1) / p.BK);
           const int lo = static_cast<int>(static_cast<long long>(n) * sp / p.splits);
           const int hi = static_cast<int>(static_cast<long long>(n) * (sp + 1) / p.splits);
           wk[x].start(lo, hi - lo);
@@ -396,85 +398,79 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           __syncwarp();
         }
         if constexpr (!KV8) {
+          // ---- bf16 rows by TMA: warp 8 the keys, warp 9 the values, a box per block and 64 columns
           for (int t = 0; t < T; ++t, ++kv_it) {
-            const uint32_t ks = kv_it % KST, vs = kv_it % VST;
-            ListWalk& w = wk[PAIR ? (t < both ? t & 1 : longer) : 0];
-            int blk[4];  // the stage's blocks (-1: none)
-            int short_rows = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              blk[i] = i < BPS ? w.next() : -1;
-              if (blk[i] >= 0 && w.len - blk[i] * p.BK < p.BK) short_rows = 1;
-            }
-            // run r (32 keys) lies in block r * 32 / BK of the stage
-            int mine = blk[0];
-#pragma unroll
-            for (int i = 1; i < 4; ++i)
-              if ((lane & 3) * 32 / p.BK == i) mine = blk[i];
-            const int valid = mine < 0 ? 0 : min(32, max(0, w.len - mine * p.BK - ((lane & 3) * 32) % p.BK));
-            int loads = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) loads += blk[i] >= 0 ? 1 : 0;
-            const uint32_t bytes = static_cast<uint32_t>(loads * p.BK) * HD * 2;
-            if (!mbar_wait_warp(k_empty + ks, ((kv_it / KST) & 1) ^ 1, abort_flag, wl)) { okp = false; break; }
-            if (lane < 4) sInfo[ks].valid[lane] = valid;
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive_expect_tx(k_full + ks, bytes);
+            int blk[4] = {-1, -1, -1, -1};  // the stage's blocks (-1: none)
+            if (PAIR && (t < both ? (t & 1) : longer)) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                if (blk[i] >= 0)
+                if (i < BPS) blk[i] = wk[PAIR ? 1 : 0].next();
+            } else {
 #pragma unroll
-                  for (int h = 0; h < HD / 64; ++h)
-                    tma_load_2d(sK + ks * L::TILE_BYTES + h * HALF + i * p.BK * 128, &tmK, h * 64,
-                                bkv * p.Nk + blk[i] * p.BK, k_full + ks);
+              for (int i = 0; i < 4; ++i)
+                if (i < BPS) blk[i] = wk[0].next();
             }
-            ++k_issued;
-            __syncwarp();
-            if (!mbar_wait_warp(v_empty + vs, ((kv_it / VST) & 1) ^ 1, abort_flag, wl)) { okp = false; break; }
-            const uint32_t dV = sV + vs * L::TILE_BYTES;
-            // masked keys weigh 0, but 0 times whatever lies in their V rows need not be 0: rows of no
-            // block are cleared beside the copies, rows behind the last valid one after theirs
-            const bool gaps = loads < BPS;
-            if (gaps) {
-              for (int r = loads * p.BK + lane; r < kTile; r += 32)
+            int loads = 0;
+            bool cut = false;  // a block reaches behind the last valid key
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              loads += blk[i] >= 0 ? 1 : 0;
+              cut |= blk[i] >= 0 && len - blk[i] * p.BK < p.BK;
+            }
+            // valid keys of run lane & 3 (32 keys, in block run * 32 / BK of the stage)
+            const int at = (lane & 3) * 32 >> bk_log;
+            const int mine = at == 0 ? blk[0] : at == 1 ? blk[1] : at == 2 ? blk[2] : blk[3];
+            const int valid = mine < 0 ? 0 : min(32, max(0, len - mine * p.BK - (((lane & 3) * 32) & (p.BK - 1))));
+            const uint32_t bytes = static_cast<uint32_t>(loads) << (bk_log + (HD == 128 ? 8 : 7));
+            auto copy = [&](uint32_t dst, const CUtensorMap* map, uint64_t* bar) {
+              if (lane == 0) {
+                mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (i < loads)
+#pragma unroll
+                    for (int h = 0; h < HD / 64; ++h)
+                      tma_load_2d(dst + h * HALF + i * p.BK * 128, map, h * 64, bkv * p.Nk + blk[i] * p.BK, bar);
+              }
+              __syncwarp();
+            };
+            if (pw == 0) {
+              const uint32_t ks = kv_it % KST;
+              if (!mbar_wait_warp(k_empty + ks, ((kv_it / KST) & 1) ^ 1, abort_flag, wl)) { okp = false; break; }
+              if (lane < 4) sInfo[ks].valid[lane] = valid;
+              __syncwarp();
+              copy(sK + ks * L::TILE_BYTES, &tmK, k_full + ks);
+            } else {
+              const uint32_t vs = kv_it % VST;
+              if (!mbar_wait_warp(v_empty + vs, ((kv_it / VST) & 1) ^ 1, abort_flag, wl)) { okp = false; break; }
+              const uint32_t dV = sV + vs * L::TILE_BYTES;
+              // masked keys weigh 0, but 0 times whatever lies in their V rows need not be 0: rows of no
+              // block are cleared beside the copies, rows behind the last valid one after theirs
+              auto clear = [&](int r) {
 #pragma unroll
                 for (int c = 0; c < HD / 8; ++c)
                   asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dV + sw128_offset(r, c, kTile)), "r"(0u)
                                : "memory");
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
-            uint64_t* land = short_rows ? vfix : v_full + vs;
-            if (lane == 0) {
-              mbar_arrive_expect_tx(land, bytes);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (blk[i] >= 0)
-#pragma unroll
-                  for (int h = 0; h < HD / 64; ++h)
-                    tma_load_2d(dV + h * HALF + i * p.BK * 128, &tmV, h * 64, bkv * p.Nk + blk[i] * p.BK, land);
-            }
-            __syncwarp();
-            if (short_rows) {
-              mbar_drain(vfix, n_fix & 1);
-              ++n_fix;
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const int vr = __shfl_sync(0xffffffffu, valid, r);
-                if (lane >= vr)
-#pragma unroll
-                  for (int c = 0; c < HD / 8; ++c)
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dV + sw128_offset(r * 32 + lane, c, kTile)),
-                                 "r"(0u)
-                                 : "memory");
+              };
+              if (loads < BPS) {
+                for (int r = loads * p.BK + lane; r < kTile; r += 32) clear(r);
+                fence_proxy_async_smem();
+                __syncwarp();
               }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(v_full + vs);
+              copy(dV, &tmV, cut ? vfix : v_full + vs);
+              if (cut) {
+                mbar_drain(vfix, n_fix & 1);
+                ++n_fix;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                  if (lane >= __shfl_sync(0xffffffffu, valid, r)) clear(r * 32 + lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(v_full + vs);
+                __syncwarp();
+              }
             }
-            ++v_issued;
-            __syncwarp();
+            ++issued;
           }
         } else {
           // ---- 8-bit rows: this warp's run of 32 keys of every stage
@@ -484,14 +480,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           float fks = 1.f, fvs = 1.f;
           int valid = 0;
           auto fetch = [&](int t) {
-            ListWalk& w = wk[PAIR ? (t < both ? t & 1 : longer) : 0];
             int mine = -1;
-            for (int i = 0; i < BPS; ++i) {
-              const int x = w.next();
-              if (pw * 32 / p.BK == i) mine = x;
-            }
+            auto walk = [&](ListWalk& w) {
+              for (int i = 0; i < BPS; ++i) {
+                const int x = w.next();
+                if (pw * 32 >> bk_log == i) mine = x;
+              }
+            };
+            if (PAIR && (t < both ? (t & 1) : longer)) walk(wk[PAIR ? 1 : 0]);
+            else walk(wk[0]);
             const int row0 = mine * p.BK + (pw * 32) % p.BK;
-            valid = mine < 0 ? 0 : min(32, max(0, w.len - row0));
+            valid = mine < 0 ? 0 : min(32, max(0, len - row0));
             fks = fvs = 1.f;
             if (mine >= 0) {
               fks = p.ks[static_cast<size_t>(bkv) * p.nb + mine];
@@ -549,18 +548,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
         }
       }
-      if (pw == 0 && !okp) {
+      if (!okp) {
         // after an abort, the TMA loads already issued land before the CTA releases its shared memory
         // (on a normal exit every load has been consumed)
         if (q_issued > 0) mbar_drain(q_full, (q_issued - 1) & 1);
         if constexpr (!KV8) {
-          for (uint32_t s = 0; s < static_cast<uint32_t>(KST) && s < k_issued; ++s) {
-            const uint32_t last = k_issued - 1 - ((k_issued - 1 + KST - s) % KST);
-            mbar_drain(k_full + s, (last / KST) & 1);
-          }
-          for (uint32_t s = 0; s < static_cast<uint32_t>(VST) && s < v_issued; ++s) {
-            const uint32_t last = v_issued - 1 - ((v_issued - 1 + VST - s) % VST);
-            mbar_drain(v_full + s, (last / VST) & 1);
+          const uint32_t ring = pw == 0 ? KST : VST;
+          uint64_t* full = pw == 0 ? k_full : v_full;
+          for (uint32_t s = 0; s < ring && s < issued; ++s) {
+            const uint32_t last = issued - 1 - ((issued - 1 + ring - s) % ring);
+            mbar_drain(full + s, (last / ring) & 1);
           }
         }
       }
@@ -680,7 +677,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (!mbar_wait_warp(s_full + x, sc & 1, abort_flag, wl)) { ok = false; break; }
           const uint32_t slot = (kv_base + stage_pos(tn, x, i)) % KST;
           const int4 v4 = *reinterpret_cast<const int4*>(sInfo[slot].valid);
-          const int vq[4] = {v4.x, v4.y, v4.z, v4.w};
           float kq[4] = {sl2, sl2, sl2, sl2}, vsq[4] = {1.f, 1.f, 1.f, 1.f};
           if (KV8) {
             const float4 a = *reinterpret_cast<const float4*>(sInfo[slot].ks);
@@ -709,7 +705,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           };
           // P = exp2(S * scale - m) of one run of 32 keys, times its V scale, in bf16 pairs, and its
           // sums over the even and the odd keys
-          auto chunk_exps = [&](const uint32_t* sr, int v, float k, float vs, float m, uint32_t* pk, float2& cs) {
+          auto chunk_exps = [&](const uint32_t* sr, float k, float vs, float m, uint32_t* pk, float2& cs) {
             cs = make_float2(0.f, 0.f);
             const float2 k2 = make_float2(k, k), nm2 = make_float2(-m, -m), v2 = make_float2(vs, vs);
 #pragma unroll
@@ -717,10 +713,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               const float2 xv =
                   __ffma2_rn(make_float2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), k2, nm2);
               float2 e = make_float2(fast_exp2(xv.x), fast_exp2(xv.y));
-              if (v < 32) {
-                e.x = 2 * c < v ? e.x : 0.f;
-                e.y = 2 * c + 1 < v ? e.y : 0.f;
-              }
               cs = __fadd2_rn(cs, e);
               if (KV8) e = __fmul2_rn(e, v2);
               pk[c] = pack_bf16x2(e.x, e.y);
@@ -735,22 +727,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           reg_fence32(sr + 32);
           reg_fence32(sr + 64);
           reg_fence32(sr + 96);
+          if ((v4.x & v4.y & v4.z & v4.w) != 32) {  // masked keys: logits of -inf, whatever was computed
+            const int vq[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+            for (int c = 0; c < kTile; ++c) sr[c] = (c & 31) < vq[c >> 5] ? sr[c] : 0xff800000u;
+          }
           // Rows without a reference yet (the first stage, or every key so far masked or at -inf; O_x
           // and l are 0 then) take the stage's exact maximum.
-          if (i == 0 || __any_sync(0xffffffffu, m_used == -INFINITY)) {
+          if (__any_sync(0xffffffffu, m_used == -INFINITY)) {
             float mx = -INFINITY;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               float a = -INFINITY, b = -INFINITY;
-              if (vq[q] >= 32) {
 #pragma unroll
-                for (int c = 0; c < 32; c += 2) {
-                  a = fmaxf(a, __uint_as_float(sr[32 * q + c]));
-                  b = fmaxf(b, __uint_as_float(sr[32 * q + c + 1]));
-                }
-              } else {
-#pragma unroll
-                for (int c = 0; c < 32; ++c) a = fmaxf(a, c < vq[q] ? __uint_as_float(sr[32 * q + c]) : -INFINITY);
+              for (int c = 0; c < 32; c += 2) {
+                a = fmaxf(a, __uint_as_float(sr[32 * q + c]));
+                b = fmaxf(b, __uint_as_float(sr[32 * q + c + 1]));
               }
               mx = fmaxf(mx, fmaxf(a, b) * kq[q]);
             }
@@ -773,7 +765,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           for (int q = 0; q < 4; ++q) {
             uint32_t pk[16];
             float2 cs;
-            chunk_exps(sr + 32 * q, vq[q], kq[q], vsq[q], m_used == -INFINITY ? 0.f : m_used, pk, cs);
+            chunk_exps(sr + 32 * q, kq[q], vsq[q], m_used == -INFINITY ? 0.f : m_used, pk, cs);
             const bool big = !(cs.x + cs.y <= 4294967296.f);  // 2^32, or inf / NaN
             if (__any_sync(0xffffffffu, big)) {
               // rare: raise this row's reference to the run's largest logit by whole octaves (so that
@@ -781,8 +773,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               const float mz = m_used == -INFINITY ? 0.f : m_used;
               float xm = -INFINITY;
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (c < vq[q]) xm = fmaxf(xm, fmaf(__uint_as_float(sr[32 * q + c]), kq[q], -mz));
+              for (int c = 0; c < 32; ++c) xm = fmaxf(xm, fmaf(__uint_as_float(sr[32 * q + c]), kq[q], -mz));
               const bool raise = big && xm > 0.f;
               const float xr = raise ? fminf(ceilf(xm), 65536.f) : 0.f;
               const int n = static_cast<int>(xr);
@@ -815,7 +806,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               }
               tmem_st_wait();
               if (raise) m_used = mz + xr;
-              chunk_exps(sr + 32 * q, vq[q], kq[q], vsq[q], m_used == -INFINITY ? 0.f : m_used, pk, cs);
+              chunk_exps(sr + 32 * q, kq[q], vsq[q], m_used == -INFINITY ? 0.f : m_used, pk, cs);
             }
             rs = __fadd2_rn(rs, cs);
             tmem_st16(tS + 16 * q, pk);
