@@ -217,8 +217,8 @@ struct BlockSmem {
   static constexpr uint32_t UNIT_OFF = INFO_OFF + KST * sizeof(StageInfo);  // stages of both streams, 4 units
   static constexpr uint32_t BAR_OFF = UNIT_OFF + 4 * 8;
   // q_full, q_empty, k_full[KST], k_empty[KST], v_full[VST], v_empty[VST]; per stream s_full, p_full,
-  // pv_done, p_half, pvlo_done; o_empty, drain, vfix, pair[4], u_full[4]
-  static constexpr int NBAR = 2 + 2 * KST + 2 * VST + 10 + 3 + 4 + 4;
+  // pv_done, p_half, pvlo_done, s_hi; o_empty, drain, vfix, pair[4], u_full[4]
+  static constexpr int NBAR = 2 + 2 * KST + 2 * VST + 12 + 3 + 4 + 4;
   static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
   static constexpr uint32_t BYTES = MISC_OFF + 16;
   static_assert(BAR_OFF % 8 == 0 && INFO_OFF % 16 == 0, "shared memory alignment");
@@ -249,9 +249,13 @@ __device__ __forceinline__ void e4m3_to_bf16(const uint4& u, uint32_t* w) {
 // from an 8-bit store, loaded to registers, widened to bf16 and stored by the four producer warps.
 //   PAIR = false  both streams work on the tile's 128 rows, alternate stages; merged at the end.
 //   PAIR = true   lists of 64 rows: stream A takes rows 0-63 with their list, stream B rows 64-127
-//                 with theirs.  The MMAs compute all 128 rows either way; each stream's two idle
-//                 warps leave its other half alone, so no exponential is spent on it, and the
-//                 active warps lie on all four sub-partitions.
+//                 with theirs.  The MMAs compute all 128 rows either way; no exponential is spent on
+//                 a stream's other half, and the active warps lie on all four sub-partitions.
+//                 d = 64: TMEM has room for four accumulators, so a stream's rows are worked on by
+//                 two warps each, the first and the last 64 keys of every stage, with a running
+//                 maximum, sum and O of their own, merged at the end like two streams (a stage's
+//                 time is its longest chain of waits and exponentials: 1.17 us with one warp a row).
+//                 d = 128: one warp a row.
 // A unit with no usable entry has one stage of 128 masked keys, so that every unit takes the same path.
 template <int HD, bool KV8, bool PAIR>
 __global__ void __launch_bounds__(kAttnThreads, 1)
@@ -261,9 +265,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   using RG = BlockRegs<KV8>;
   constexpr int KST = L::KST, VST = L::VST;
   constexpr uint32_t HALF = kTile * 128;
-  constexpr uint32_t IDESC_QK = idesc_bf16(128, kTile, false, false);
+  constexpr bool SUB = PAIR && HD == 64;               // a stream's keys in two halves, a warp pair each
+  constexpr uint32_t ACTIVE = PAIR && !SUB ? 64 : 128;  // softmax threads of a stream
+  constexpr int RUNS = SUB ? 2 : 4;                     // runs of 32 keys that a softmax thread takes
+  constexpr int ISSUERS = SUB ? 4 : PAIR ? 2 : 1;       // MMA-issuing warps
+  constexpr uint32_t IDESC_QK = idesc_bf16(128, 32 * RUNS, false, false);
   constexpr uint32_t IDESC_PV = idesc_bf16(128, HD, false, true);
-  constexpr uint32_t ACTIVE = PAIR ? 64 : 128;  // softmax threads of a stream
   constexpr uint32_t LAUNCH_REGS = 65536 / kAttnThreads;
 
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -279,12 +286,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint64_t* k_empty = k_full + KST;
   uint64_t* v_full = k_empty + KST;
   uint64_t* v_empty = v_full + VST;
-  uint64_t* s_full = v_empty + VST;  // [2], per stream, as the next four
+  uint64_t* s_full = v_empty + VST;  // [2], per stream, as the next five
   uint64_t* p_full = s_full + 2;
   uint64_t* pv_done = p_full + 2;
   uint64_t* p_half = pv_done + 2;
   uint64_t* pvlo_done = p_half + 2;
-  uint64_t* o_empty = pvlo_done + 2;
+  uint64_t* s_hi = pvlo_done + 2;  // SUB: S of a stage's second half (s_full: of its first)
+  uint64_t* o_empty = s_hi + 2;
   uint64_t* drain = o_empty + 1;
   uint64_t* vfix = drain + 1;    // V stage whose last rows are cleared before it is handed on
   uint64_t* pair = vfix + 1;     // [4], one per row group (its two warps)
@@ -301,24 +309,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, ISSUERS);
     for (int s = 0; s < KST; ++s) {
       mbar_init(k_full + s, KV8 ? 128 : 1);
       mbar_init(k_empty + s, ACTIVE);
     }
     for (int s = 0; s < VST; ++s) {
       mbar_init(v_full + s, KV8 ? 128 : 1);
-      mbar_init(v_empty + s, 1);
+      mbar_init(v_empty + s, SUB ? 2 : 1);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(s_full + x, 1);
-      mbar_init(p_full + x, ACTIVE);
+      mbar_init(s_hi + x, 1);
+      mbar_init(p_full + x, SUB ? 64 : ACTIVE);
       mbar_init(pv_done + x, 1);
-      mbar_init(p_half + x, ACTIVE);
+      mbar_init(p_half + x, SUB ? 64 : ACTIVE);
       mbar_init(pvlo_done + x, 1);
     }
     mbar_init(o_empty, 2 * ACTIVE);
-    mbar_init(drain, 1);
+    mbar_init(drain, ISSUERS);
     mbar_init(vfix, 1);
     for (int g = 0; g < 4; ++g) mbar_init(pair + g, 64);
     for (int g = 0; g < 4; ++g) mbar_init(u_full + g, 1);
@@ -565,13 +574,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   } else if (warp >= 12) {
     // ------------------------------------------------------------------ MMA issuer
     regs_to<RG::MMA, LAUNCH_REGS>();
-    if (warp == 12) {
+    if (warp < 12 + ISSUERS) {
       const uint64_t dQ = desc_sw128(sQ, 16, 1024);
       const uint64_t dK0 = desc_sw128(sK, 16, 1024);
       const uint64_t dV0 = desc_sw128(sV, HALF, 1024);
       constexpr uint64_t kSlotStep = L::TILE_BYTES >> 4;
       uint32_t kv_base = 0, u_it = 0;
-      uint32_t sc0 = 0, sc1 = 0;  // PVs issued per stream (barrier phases)
       bool ok = true;
       if (p.hold != nullptr) {
         if (lane == 0) {
@@ -587,79 +595,130 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
-      for (int unit = blockIdx.x; unit < p.num_units && ok; unit += gridDim.x, ++u_it) {
-        ok = mbar_wait_warp(u_full + (u_it & 3), (u_it >> 2) & 1, abort_flag, wl);
-        if (!ok) break;
-        const int2 tn = sUnit[u_it & 3];
-        const int T = tn.x + tn.y, both = 2 * min(tn.x, tn.y), longer = tn.x >= tn.y ? 0 : 1;
-        ok = mbar_wait_warp(q_full, u_it & 1, abort_flag, wl);
-        if (!ok) break;
-        auto qk_mmas = [&](int t, int x) {  // S_x of the stage at place t
-          const uint32_t ks = (kv_base + t) % KST;
-          const uint64_t dK = dK0 + ks * kSlotStep;
-          const uint32_t dS = tmem + kTmS + x * kTile;
+      auto wait_k = [&](int t) -> bool {
+        const uint32_t it = kv_base + t;
+        return mbar_wait_warp(k_full + it % KST, (it / KST) & 1, abort_flag, wl);
+      };
+      auto wait_v = [&](int t) -> bool {
+        const uint32_t it = kv_base + t;
+        return mbar_wait_warp(v_full + it % VST, (it / VST) & 1, abort_flag, wl);
+      };
+      // S_x of the stage at place t (SUB: of its half h)
+      auto qk_mmas = [&](int t, int x, int h) {
+        const uint32_t ks = (kv_base + t) % KST;
+        const uint64_t dK = dK0 + ks * kSlotStep + h * (64 * 128 >> 4);
+        const uint32_t dS = tmem + kTmS + x * kTile + h * 64;
 #pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk) {
-            const uint64_t koff = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
-            mma_bf16_ss_warp(dS, dQ + koff, dK + koff, IDESC_QK, kk > 0 ? 1u : 0u);
-          }
-          mma_commit_warp(s_full + x);
-          if (t == T - 1) mma_commit_warp(q_empty);
-        };
-        auto wait_k = [&](int t) -> bool {
-          const uint32_t it = kv_base + t;
-          return mbar_wait_warp(k_full + it % KST, (it / KST) & 1, abort_flag, wl);
-        };
-        // the first stage of each stream: places 0 and 1 (place 1 of a lone stream A waits its turn)
-        ok = wait_k(0) && (both == 0 || wait_k(1));
-        if (!ok) break;
-        qk_mmas(0, 0);
-        if (both > 0) qk_mmas(1, 1);
-        int n0 = 0, n1 = 0;  // stages of each stream done in this unit
-        for (int t = 0; t < T && ok; ++t) {
-          const int x = t < both ? t & 1 : longer;
-          const int mine = x ? n1 : n0;  // which stage of its stream
-          const bool next = mine + 1 < (x ? tn.y : tn.x);
-          const int tnext = next ? stage_pos(tn, x, mine + 1) : 0;
-          const uint32_t it = kv_base + t, vs = it % VST;
-          ok = mbar_wait_warp(p_half + x, (x ? sc1 : sc0) & 1, abort_flag, wl) &&
-               mbar_wait_warp(v_full + vs, (it / VST) & 1, abort_flag, wl) &&
-               (t != 0 || mbar_wait_warp(o_empty, (u_it & 1) ^ 1, abort_flag, wl));
-          if (!ok) break;
-          tc_fence_after();  // P_x was written by tcgen05.st of the softmax
-          const uint64_t dV = dV0 + vs * kSlotStep;
-          const uint32_t tO = tmem + kTmO + x * HD, tP = tmem + kTmS + x * kTile;
-          const bool first = mine == 0;  // overwrites O_x
-#pragma unroll
-          for (int kk = 0; kk < 2 * kPSplit; ++kk)
-            mma_bf16_ts_warp(tO, tP + kk * 8, dV + kk * (2048 >> 4), IDESC_PV, (!first || kk > 0) ? 1u : 0u);
-          mma_commit_warp(pvlo_done + x);
-          ok = mbar_wait_warp(p_full + x, (x ? sc1 : sc0) & 1, abort_flag, wl) && (!next || wait_k(tnext));
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 2 * kPSplit; kk < kTile / 16; ++kk)
-            mma_bf16_ts_warp(tO, tP + kk * 8, dV + kk * (2048 >> 4), IDESC_PV, 1u);
-          mma_commit_warp(pv_done + x);
-          mma_commit_warp(v_empty + vs);
-          if (x) ++sc1, ++n1;
-          else ++sc0, ++n0;
-          if (next) qk_mmas(tnext, x);
+        for (int kk = 0; kk < HD / 16; ++kk) {
+          const uint64_t koff = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+          mma_bf16_ss_warp(dS, dQ + koff, dK + koff, IDESC_QK, kk > 0 ? 1u : 0u);
         }
-        kv_base += T;
+        mma_commit_warp((h ? s_hi : s_full) + x);
+      };
+      // k steps [from, to) of O += P V for the stage at place t
+      auto pv_mmas = [&](int t, int x, int h, int from, int to, bool first) {
+        const uint64_t dV = dV0 + ((kv_base + t) % VST) * kSlotStep + h * (4 * 2048 >> 4);
+        const uint32_t tO = tmem + kTmO + (SUB ? 2 * x + h : x) * HD, tP = tmem + kTmS + x * kTile + h * 64;
+#pragma unroll
+        for (int kk = from; kk < to; ++kk)
+          mma_bf16_ts_warp(tO, tP + kk * 8, dV + kk * (2048 >> 4), IDESC_PV, (!first || kk > 0) ? 1u : 0u);
+      };
+      if constexpr (PAIR) {
+        // one warp for each stream (SUB: and half of its keys), which waits for nothing of the others
+        const int x = (warp - 12) & 1, h = (warp - 12) >> 1;
+        uint32_t sc = 0;  // PVs issued (barrier phases)
+        for (int unit = blockIdx.x; unit < p.num_units && ok; unit += gridDim.x, ++u_it) {
+          ok = mbar_wait_warp(u_full + (u_it & 3), (u_it >> 2) & 1, abort_flag, wl);
+          if (!ok) break;
+          const int2 tn = sUnit[u_it & 3];
+          const int Tx = x ? tn.y : tn.x;
+          ok = mbar_wait_warp(q_full, u_it & 1, abort_flag, wl) && (Tx == 0 || wait_k(stage_pos(tn, x, 0)));
+          if (!ok) break;
+          if (Tx > 0) qk_mmas(stage_pos(tn, x, 0), x, h);
+          if (Tx <= 1) mma_commit_warp(q_empty);
+          for (int i = 0; i < Tx; ++i, ++sc) {
+            const int t = stage_pos(tn, x, i);
+            const bool next = i + 1 < Tx;
+            const int tnext = next ? stage_pos(tn, x, i + 1) : 0;
+            ok = (!next || wait_k(tnext)) && wait_v(t) &&
+                 (i != 0 || mbar_wait_warp(o_empty, (u_it & 1) ^ 1, abort_flag, wl)) &&
+                 mbar_wait_warp((SUB && h == 1 ? p_full : p_half) + x, sc & 1, abort_flag, wl);
+            if (!ok) break;
+            tc_fence_after();  // P_x was written by tcgen05.st of the softmax
+            if constexpr (SUB) {
+              pv_mmas(t, x, h, 0, 4, i == 0);
+              mma_commit_warp((h ? pv_done : pvlo_done) + x);
+            } else {
+              pv_mmas(t, x, 0, 0, 2 * kPSplit, i == 0);
+              mma_commit_warp(pvlo_done + x);
+              ok = mbar_wait_warp(p_full + x, sc & 1, abort_flag, wl);
+              if (!ok) break;
+              tc_fence_after();
+              pv_mmas(t, x, 0, 2 * kPSplit, kTile / 16, false);
+              mma_commit_warp(pv_done + x);
+            }
+            mma_commit_warp(v_empty + (kv_base + t) % VST);
+            if (next) {
+              qk_mmas(tnext, x, h);
+              if (i + 2 == Tx) mma_commit_warp(q_empty);
+            }
+          }
+          kv_base += tn.x + tn.y;
+        }
+      } else {
+        uint32_t sc0 = 0, sc1 = 0;  // PVs issued per stream (barrier phases)
+        for (int unit = blockIdx.x; unit < p.num_units && ok; unit += gridDim.x, ++u_it) {
+          ok = mbar_wait_warp(u_full + (u_it & 3), (u_it >> 2) & 1, abort_flag, wl);
+          if (!ok) break;
+          const int2 tn = sUnit[u_it & 3];
+          const int T = tn.x + tn.y;  // stages alternate between the streams
+          ok = mbar_wait_warp(q_full, u_it & 1, abort_flag, wl) && wait_k(0) && (T < 2 || wait_k(1));
+          if (!ok) break;
+          qk_mmas(0, 0, 0);
+          if (T > 1) qk_mmas(1, 1, 0);
+          if (T <= 2) mma_commit_warp(q_empty);
+          for (int t = 0; t < T && ok; ++t) {
+            const int x = t & 1;
+            const bool next = t + 2 < T;
+            ok = mbar_wait_warp(p_half + x, (x ? sc1 : sc0) & 1, abort_flag, wl) && wait_v(t) &&
+                 (t != 0 || mbar_wait_warp(o_empty, (u_it & 1) ^ 1, abort_flag, wl));
+            if (!ok) break;
+            tc_fence_after();  // P_x was written by tcgen05.st of the softmax
+            pv_mmas(t, x, 0, 0, 2 * kPSplit, t < 2);
+            mma_commit_warp(pvlo_done + x);
+            ok = mbar_wait_warp(p_full + x, (x ? sc1 : sc0) & 1, abort_flag, wl) && (!next || wait_k(t + 2));
+            if (!ok) break;
+            tc_fence_after();
+            pv_mmas(t, x, 0, 2 * kPSplit, kTile / 16, false);
+            mma_commit_warp(pv_done + x);
+            mma_commit_warp(v_empty + (kv_base + t) % VST);
+            if (x) ++sc1;
+            else ++sc0;
+            if (next) {
+              qk_mmas(t + 2, x, 0);
+              if (t + 3 == T) mma_commit_warp(q_empty);
+            }
+          }
+          kv_base += T;
+        }
       }
+      // every MMA issued above has completed before TMEM is released
       mma_commit_warp(drain);
       mbar_drain(drain, 0);
-    }  // warps 13-15 only complete the warpgroup
+    }  // the other warps only complete the warpgroup
   } else {
     // ------------------------------------------------------------------ softmax + epilogue
     regs_to<RG::SOFTMAX, LAUNCH_REGS>();
-    const int rg = warp & 3, x = warp >> 2;  // row group, stream
-    if (!PAIR || (rg >> 1) == x) {
+    const int rg = warp & 3, side = warp >> 2;  // row group, first or second of its two warps
+    const int x = SUB ? rg >> 1 : side;         // stream
+    if (!PAIR || SUB || (rg >> 1) == x) {
       const int row = rg * 32 + lane;  // tile row == TMEM lane
       const uint32_t lane_base = static_cast<uint32_t>(rg * 32) << 16;
-      const uint32_t tS = tmem + lane_base + kTmS + x * kTile;
-      const uint32_t tOx = tmem + lane_base + kTmO + x * HD;
+      const int r0 = SUB ? 2 * side : 0;  // this thread's first run of a stage
+      const uint32_t tS = tmem + lane_base + kTmS + x * kTile + r0 * 32;
+      const uint32_t tOx = tmem + lane_base + kTmO + (SUB ? 2 * x + side : x) * HD;
+      uint64_t* s_mine = SUB && side == 1 ? s_hi + x : s_full + x;
+      uint64_t* pv_mine = SUB && side == 0 ? pvlo_done + x : pv_done + x;  // the last PV of this thread's P
       const float sl2 = p.scale_log2;
       uint32_t sc = 0, kv_base = 0, u_it = 0;
       bool ok = true;
@@ -674,15 +733,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         float m_used = -INFINITY, l_part = 0.f;  // -inf: no key of weight yet
         float m_pend = -INFINITY;  // a raise of the reference decided by the stream's previous stage
         for (int i = 0; i < Tx; ++i, ++sc) {
-          if (!mbar_wait_warp(s_full + x, sc & 1, abort_flag, wl)) { ok = false; break; }
+          if (!mbar_wait_warp(s_mine, sc & 1, abort_flag, wl)) { ok = false; break; }
           const uint32_t slot = (kv_base + stage_pos(tn, x, i)) % KST;
-          const int4 v4 = *reinterpret_cast<const int4*>(sInfo[slot].valid);
-          float kq[4] = {sl2, sl2, sl2, sl2}, vsq[4] = {1.f, 1.f, 1.f, 1.f};
-          if (KV8) {
-            const float4 a = *reinterpret_cast<const float4*>(sInfo[slot].ks);
-            const float4 b = *reinterpret_cast<const float4*>(sInfo[slot].vs);
-            kq[0] *= a.x, kq[1] *= a.y, kq[2] *= a.z, kq[3] *= a.w;
-            vsq[0] = b.x, vsq[1] = b.y, vsq[2] = b.z, vsq[3] = b.w;
+          int vq[RUNS], all = 32;
+          float kq[RUNS], vsq[RUNS];
+#pragma unroll
+          for (int q = 0; q < RUNS; ++q) {
+            vq[q] = sInfo[slot].valid[r0 + q];
+            all &= vq[q];
+            kq[q] = KV8 ? sl2 * sInfo[slot].ks[r0 + q] : sl2;
+            vsq[q] = KV8 ? sInfo[slot].vs[r0 + q] : 1.f;
           }
           // the QK^T that wrote S has read its K slot: hand the slot back to the producer
           mbar_arrive(k_empty + slot);
@@ -718,26 +778,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               pk[c] = pack_bf16x2(e.x, e.y);
             }
           };
-          uint32_t sr[128];
-          tmem_ld32(tS, sr);
-          tmem_ld32(tS + 32, sr + 32);
-          tmem_ld32(tS + 64, sr + 64);
-          tmem_ld32(tS + 96, sr + 96);
-          tmem_ld_wait_regs(sr);
-          reg_fence32(sr + 32);
-          reg_fence32(sr + 64);
-          reg_fence32(sr + 96);
-          if ((v4.x & v4.y & v4.z & v4.w) != 32) {  // masked keys: logits of -inf, whatever was computed
-            const int vq[4] = {v4.x, v4.y, v4.z, v4.w};
+          uint32_t sr[32 * RUNS];
 #pragma unroll
-            for (int c = 0; c < kTile; ++c) sr[c] = (c & 31) < vq[c >> 5] ? sr[c] : 0xff800000u;
+          for (int q = 0; q < RUNS; ++q) tmem_ld32(tS + 32 * q, sr + 32 * q);
+          tmem_ld_wait_regs(sr);
+#pragma unroll
+          for (int q = 1; q < RUNS; ++q) reg_fence32(sr + 32 * q);
+          if (all != 32) {  // masked keys: logits of -inf, whatever was computed
+#pragma unroll
+            for (int c = 0; c < 32 * RUNS; ++c) sr[c] = (c & 31) < vq[c >> 5] ? sr[c] : 0xff800000u;
           }
           // Rows without a reference yet (the first stage, or every key so far masked or at -inf; O_x
           // and l are 0 then) take the stage's exact maximum.
           if (__any_sync(0xffffffffu, m_used == -INFINITY)) {
             float mx = -INFINITY;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < RUNS; ++q) {
               float a = -INFINITY, b = -INFINITY;
 #pragma unroll
               for (int c = 0; c < 32; c += 2) {
@@ -751,7 +807,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           // A stage whose P summed past 2^16 raised the reference for this one, applied once the
           // stream's previous PV has completed so that O_x and l follow.
           if (__any_sync(0xffffffffu, m_pend > m_used)) {
-            if (!mbar_wait_warp(pv_done + x, (sc - 1) & 1, abort_flag, wl)) { ok = false; break; }
+            if (!mbar_wait_warp(pv_mine, (sc - 1) & 1, abort_flag, wl)) { ok = false; break; }
             tc_fence_after();
             const float alpha = m_pend > m_used ? fast_exp2(m_used - m_pend) : 1.f;
             rescale_o(alpha);
@@ -762,7 +818,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           // known complete: the stream's previous PV (o_prev), also this stage's first part (o_lo)
           bool o_prev = false, o_lo = false;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < RUNS; ++q) {
             uint32_t pk[16];
             float2 cs;
             chunk_exps(sr + 32 * q, kq[q], vsq[q], m_used == -INFINITY ? 0.f : m_used, pk, cs);
@@ -778,12 +834,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               const float xr = raise ? fminf(ceilf(xm), 65536.f) : 0.f;
               const int n = static_cast<int>(xr);
               const float alpha = n >= 127 ? 0.f : __int_as_float((127 - n) << 23);  // 2^-n
-              if (q >= kPSplit && !o_lo) {
+              if (!SUB && q >= kPSplit && !o_lo) {
                 if (!mbar_wait_warp(pvlo_done + x, sc & 1, abort_flag, wl)) { ok = false; break; }
                 tc_fence_after();
                 o_lo = o_prev = true;
               } else if (!o_prev) {
-                if (!mbar_wait_warp(pv_done + x, (sc - 1) & 1, abort_flag, wl)) { ok = false; break; }
+                if (!mbar_wait_warp(pv_mine, (sc - 1) & 1, abort_flag, wl)) { ok = false; break; }
                 tc_fence_after();
                 o_prev = true;
               }
@@ -793,7 +849,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               rs.x *= alpha;
               rs.y *= alpha;
 #pragma unroll 1
-              for (int q2 = q >= kPSplit ? kPSplit : 0; q2 < q; ++q2) {
+              for (int q2 = !SUB && q >= kPSplit ? kPSplit : 0; q2 < q; ++q2) {
                 uint32_t pv[16];
                 tmem_ld16(tS + 16 * q2, pv);
                 tmem_ld_wait_regs16(pv);
@@ -810,7 +866,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             rs = __fadd2_rn(rs, cs);
             tmem_st16(tS + 16 * q, pk);
-            if (q == kPSplit - 1) signal_half();
+            if (!SUB && q == kPSplit - 1) signal_half();
           }
           if (!ok) break;
           const float st = rs.x + rs.y;
@@ -818,7 +874,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           l_part += st;
           tmem_st_wait();
           tc_fence_before();
-          mbar_arrive(p_full + x);
+          mbar_arrive(SUB && side == 0 ? p_half + x : p_full + x);
         }
         if (!ok) break;
         kv_base += tn.x + tn.y;
@@ -826,7 +882,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const size_t prow = static_cast<size_t>(sp) * p.B * p.H * p.Nq + orow;  // of a split's partial result
         if (Tx > 0) {
           // this stream's last PV of the unit
-          if (!mbar_wait_warp(pv_done + x, (sc - 1) & 1, abort_flag, wl)) { ok = false; break; }
+          if (!mbar_wait_warp(pv_mine, (sc - 1) & 1, abort_flag, wl)) { ok = false; break; }
           tc_fence_after();
         }
         // 8 output columns from column c on: R is added, or the partial result goes to the workspace
@@ -841,7 +897,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         };
         const bool add = live && p.R != nullptr && p.splits == 1;
         float m_all = m_used, l_sum = l_part;
-        if constexpr (PAIR) {
+        if constexpr (PAIR && !SUB) {
           const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
 #pragma unroll 1
           for (int c0 = 0; c0 < HD; c0 += 64) {
@@ -864,13 +920,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
         } else {
           constexpr int NV = HD / 16;  // uint4 (8 bf16) per half row
-          const int cx = x * (HD / 2);
+          const int cx = side * (HD / 2);
           uint4 extra[NV];
 #pragma unroll
           for (int e = 0; e < NV; ++e)
             extra[e] = add ? *reinterpret_cast<const uint4*>(p.R + orow * HD + cx + 8 * e) : make_uint4(0u, 0u, 0u, 0u);
-          const bool has_b = tn.y > 0;
-          sXch[x * kTile + row] = make_float2(m_used, l_part);
+          const bool has_b = SUB || tn.y > 0;
+          sXch[side * kTile + row] = make_float2(m_used, l_part);
           tc_fence_before();
           mbar_arrive(pair + rg);
           if (!mbar_wait_warp(pair + rg, 0, abort_flag, wl)) { ok = false; break; }
@@ -885,7 +941,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           l_sum = xa.y * wA + xb.y * wB;
           const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
           const float cA = wA * inv, cB = wB * inv;
-          const uint32_t tOA = tmem + lane_base + kTmO + cx, tOB = tOA + HD;
+          const uint32_t tOA = tmem + lane_base + kTmO + (SUB ? 2 * x * HD : 0) + cx, tOB = tOA + HD;
           uint32_t oab[HD];  // [0, HD/2): O_A; [HD/2, HD): O_B
           if constexpr (HD == 128) tmem_ld32x4_wait(tOA, tOA + 32, tOB, tOB + 32, oab);
           else tmem_ld32x2_wait(tOA, tOB, oab);
@@ -904,7 +960,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
           }
         }
-        if (live && (PAIR || x == 0)) {
+        if (live && ((PAIR && !SUB) || side == 0)) {
           const float l2 = l_sum == 0.f ? -INFINITY : m_all + __log2f(l_sum);
           if (p.splits > 1) p.plse[prow] = l2;
           else if (p.lse != nullptr) p.lse[orow] = l2 * 0.69314718055994531f;
