@@ -132,69 +132,83 @@ __global__ void __launch_bounds__(kSimpleWarps * 32) block_attn_simple_kernel(co
 
 // ---------------------------------------------------------------------------------- tensor-core form
 // A warp's walk over the usable entries of one list: block numbers within the store that hold a valid
-// key, up to the first negative entry.  32 entries at a time, the next 32 fetched ahead.
+// key, up to the first negative entry.  Lane l holds the l-th usable entry at hand, so that a stage's
+// blocks are one shuffle away; 28 raw entries at a time are packed behind the (at most three) left
+// over, with the next 28 fetched ahead.
 struct ListWalk {
+  static constexpr int WINDOW = 28;
   const int32_t* list;  // nullable: every block in turn
-  int kb, nb, BK, len;
-  int w0, id, nid, left;  // first entry of the window, this lane's entry, the next window's, entries to go
-  uint32_t mask;          // usable entries of the window not taken yet
-  bool end;               // a negative entry lies in the window (or the list is over)
+  int kb, nb, bk_log, len;
+  int w0, raw;          // next window's first entry, and this lane's entry of it
+  int cur, have, at;    // this lane's packed entry; how many there are; how many are taken
+  bool end;             // no further window
 
-  __device__ __forceinline__ int fetch(int w) const {
-    const int i = w + static_cast<int>(lane_id());
-    return i >= kb ? -1 : list != nullptr ? list[i] : i;
+  __device__ __forceinline__ int fetch() const {
+    const int l = lane_id(), i = w0 + l;
+    return l >= WINDOW || i >= kb ? -1 : list != nullptr ? list[i] : i;
   }
-  __device__ __forceinline__ void window(bool report) {
-    id = nid;
-    const uint32_t neg = __ballot_sync(0xffffffffu, id < 0);
-    const int upto = neg ? __ffs(neg) - 1 : 32;
+  // Usable lanes of the fetched window; moves on to the next.
+  __device__ __forceinline__ uint32_t window(bool report) {
+    constexpr uint32_t FULL = (1u << WINDOW) - 1u;
+    const uint32_t neg = __ballot_sync(0xffffffffu, raw < 0) & FULL;
+    const int upto = neg ? __ffs(neg) - 1 : WINDOW;
     const bool in = static_cast<int>(lane_id()) < upto;
-    if (report && in && id >= nb) raise_status(kStatusBadIndex);
-    mask = __ballot_sync(0xffffffffu, in && id < nb && static_cast<long long>(id) * BK < len);
+    if (report && in && raw >= nb) raise_status(kStatusBadIndex);
+    const uint32_t mask = __ballot_sync(0xffffffffu, in && raw < nb && (static_cast<long long>(raw) << bk_log) < len);
     end = neg != 0;
-    if (!end) nid = fetch(w0 + 32);
+    w0 += WINDOW;
+    return mask;
+  }
+  __device__ __forceinline__ void begin() {
+    w0 = have = at = 0;
+    end = false;
+    raw = fetch();
   }
   // Usable entries of the whole list.
   __device__ __forceinline__ int count(bool report) {
     int n = 0;
-    w0 = 0;
-    nid = fetch(0);
-    for (;;) {
-      window(report);
-      n += __popc(mask);
-      if (end) return n;
-      w0 += 32;
+    begin();
+    while (!end) {
+      n += __popc(window(report));
+      if (!end) raw = fetch();
+    }
+    return n;
+  }
+  __device__ __forceinline__ void refill() {
+    const int id = raw;
+    uint32_t mask = window(false);
+    if (!end) raw = fetch();
+    const int left = have - at, n = __popc(mask);
+    // the entry of rank l - left among the window's usable ones: its lane by halving
+    int rank = static_cast<int>(lane_id()) - left, src = 0;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) {
+      const int c = __popc((mask >> src) & ((1u << s) - 1u));
+      if (rank >= c) rank -= c, src += s;
+    }
+    const int old = __shfl_sync(0xffffffffu, cur, (at + static_cast<int>(lane_id())) & 31);
+    const int fresh = __shfl_sync(0xffffffffu, id, src & 31);
+    cur = static_cast<int>(lane_id()) < left ? old : fresh;
+    have = left + n;
+    at = 0;
+  }
+  // Start at usable entry `lo`.
+  __device__ __forceinline__ void start(int lo) {
+    cur = 0;
+    begin();
+    while (lo > 0) {
+      const int n = min(lo, have - at);
+      at += n;
+      lo -= n;
+      if (lo > 0) {
+        if (end) return;
+        refill();
+      }
     }
   }
-  // Start again at usable entry `lo`, to take `n` of them.
-  __device__ __forceinline__ void start(int lo, int n) {
-    left = n;
-    mask = 0;
-    if (n <= 0) return;
-    w0 = 0;
-    nid = fetch(0);
-    for (;;) {
-      window(false);
-      const int c = __popc(mask);
-      if (lo < c) break;
-      lo -= c;
-      if (end) break;
-      w0 += 32;
-    }
-    for (; lo > 0; --lo) mask &= mask - 1;
-  }
-  // The next block, or -1.
-  __device__ __forceinline__ int next() {
-    if (left <= 0) return -1;
-    --left;
-    while (mask == 0) {
-      if (end) return -1;
-      w0 += 32;
-      window(false);
-    }
-    const int l = __ffs(mask) - 1;
-    mask &= mask - 1;
-    return __shfl_sync(0xffffffffu, id, l);
+  // Have `n` <= 4 entries at hand if the list has them.
+  __device__ __forceinline__ void ensure(int n) {
+    while (have - at < n && !end) refill();
   }
 };
 
@@ -217,8 +231,8 @@ struct BlockSmem {
   static constexpr uint32_t UNIT_OFF = INFO_OFF + KST * sizeof(StageInfo);  // stages of both streams, 4 units
   static constexpr uint32_t BAR_OFF = UNIT_OFF + 4 * 8;
   // q_full, q_empty, k_full[KST], k_empty[KST], v_full[VST], v_empty[VST]; per stream s_full, p_full,
-  // pv_done, p_half, pvlo_done, s_hi; o_empty, drain, vfix, pair[4], u_full[4]
-  static constexpr int NBAR = 2 + 2 * KST + 2 * VST + 12 + 3 + 4 + 4;
+  // pv_done, p_half, pvlo_done, s_hi; o_empty, drain, vfix[2], pair[4], u_full[4]
+  static constexpr int NBAR = 2 + 2 * KST + 2 * VST + 12 + 4 + 4 + 4;
   static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
   static constexpr uint32_t BYTES = MISC_OFF + 16;
   static_assert(BAR_OFF % 8 == 0 && INFO_OFF % 16 == 0, "shared memory alignment");
@@ -268,7 +282,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   constexpr bool SUB = PAIR && HD == 64;               // a stream's keys in two halves, a warp pair each
   constexpr uint32_t ACTIVE = PAIR && !SUB ? 64 : 128;  // softmax threads of a stream
   constexpr int RUNS = SUB ? 2 : 4;                     // runs of 32 keys that a softmax thread takes
-  constexpr int ISSUERS = SUB ? 4 : PAIR ? 2 : 1;       // MMA-issuing warps
+  constexpr int ISSUERS = SUB ? 4 : 1;                  // MMA-issuing warps
+  static_assert(!SUB || (KST == VST && KST % 2 == 0), "SUB: each stream has half the slots");
   constexpr uint32_t IDESC_QK = idesc_bf16(128, 32 * RUNS, false, false);
   constexpr uint32_t IDESC_PV = idesc_bf16(128, HD, false, true);
   constexpr uint32_t LAUNCH_REGS = 65536 / kAttnThreads;
@@ -294,8 +309,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint64_t* s_hi = pvlo_done + 2;  // SUB: S of a stage's second half (s_full: of its first)
   uint64_t* o_empty = s_hi + 2;
   uint64_t* drain = o_empty + 1;
-  uint64_t* vfix = drain + 1;    // V stage whose last rows are cleared before it is handed on
-  uint64_t* pair = vfix + 1;     // [4], one per row group (its two warps)
+  uint64_t* vfix = drain + 1;    // [2]: V stage whose last rows are cleared before it is handed on
+  uint64_t* pair = vfix + 2;     // [4], one per row group (its two warps)
   uint64_t* u_full = pair + 4;   // [4], unit counts published
   StageInfo* sInfo = reinterpret_cast<StageInfo*>(smem_raw + L::INFO_OFF);
   int2* sUnit = reinterpret_cast<int2*>(smem_raw + L::UNIT_OFF);
@@ -329,8 +344,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     mbar_init(o_empty, 2 * ACTIVE);
     mbar_init(drain, ISSUERS);
     mbar_init(vfix, 1);
+    mbar_init(vfix + 1, 1);
     for (int g = 0; g < 4; ++g) mbar_init(pair + g, 64);
-    for (int g = 0; g < 4; ++g) mbar_init(u_full + g, 1);
+    for (int g = 0; g < 4; ++g) mbar_init(u_full + g, SUB && !KV8 ? 2 : 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -354,222 +370,249 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // ------------------------------------------------------------------ producer
     regs_to<RG::PRODUCER, LAUNCH_REGS>();
     const int pw = warp - 8;
-    if (KV8 || pw < 2) {
-      const int BPS = kTile / p.BK;  // blocks of a stage
-      const int bk_log = 31 - __clz(p.BK);
-      uint32_t kv_it = 0, u_it = 0, q_issued = 0, issued = 0, n_fix = 0;
-      bool okp = true;
-      for (int unit = blockIdx.x; unit < p.num_units && okp; unit += gridDim.x, ++u_it) {
-        const int sp = unit % p.splits, tu = unit / p.splits;
-        const int bh = tu / p.tiles, ut = tu - bh * p.tiles;
-        const int b = bh / p.H, bkv = b * p.Hkv + (bh - b * p.H) / (p.H / p.Hkv);
-        const int len = valid_rows(p.len, b, p.Nk);
-        ListWalk wk[PAIR ? 2 : 1];
-        int tn[2] = {0, 0};
+    const int BPS = kTile / p.BK;  // blocks of a stage
+    const int bk_log = 31 - __clz(p.BK);
+    uint32_t u_it = 0;
+    bool okp = true;
+    // What a producer warp learns of a unit: the walks over its lists, at their first entries, the
+    // entries to take of each, and so the stages of both streams (`only` >= 0: of that list's alone).
+    constexpr int LISTS = PAIR ? 2 : 1;
+    struct Unit {
+      int bh, ut, bkv, len;
+      int left[LISTS], tn[2];
+    };
+    ListWalk wk[LISTS];
+    auto open_unit = [&](int unit, int only, bool report) {
+      Unit u;
+      const int sp = unit % p.splits, tu = unit / p.splits;
+      u.bh = tu / p.tiles;
+      u.ut = tu - u.bh * p.tiles;
+      const int b = u.bh / p.H;
+      u.bkv = b * p.Hkv + (u.bh - b * p.H) / (p.H / p.Hkv);
+      u.len = valid_rows(p.len, b, p.Nk);
+      u.tn[0] = u.tn[1] = 0;
+      auto open_list = [&](ListWalk& w, int x, int& left) {
+        const int g = PAIR ? 2 * u.ut + x : u.ut;
+        const bool some = g < p.GQ;  // not so: an odd last list, stream B has no rows here
+        w.list = some && p.blocks != nullptr ? p.blocks + (static_cast<size_t>(u.bh) * p.GQ + g) * p.kb : nullptr;
+        w.kb = some ? p.kb : 0;
+        w.nb = p.nb;
+        w.bk_log = bk_log;
+        w.len = u.len;
+        const int n = p.blocks != nullptr ? w.count(report) : min(p.nb, (u.len + p.BK - 1) >> bk_log);
+        const int lo = static_cast<int>(static_cast<long long>(n) * sp / p.splits);
+        left = static_cast<int>(static_cast<long long>(n) * (sp + 1) / p.splits) - lo;
+        w.start(lo);
+        return some ? max(1, (left + BPS - 1) / BPS) : 0;
+      };
+      if (only >= 0) {
+        u.tn[only] = open_list(wk[0], only, u.left[0]);
+      } else {
 #pragma unroll
-        for (int x = 0; x < (PAIR ? 2 : 1); ++x) {
-          const int g = PAIR ? 2 * ut + x : ut;
-          wk[x].kb = p.kb;
-          wk[x].nb = p.nb;
-          wk[x].BK = p.BK;
-          wk[x].len = len;
-          if (g >= p.GQ) {  // an odd last list: stream B has no rows here
-            wk[x].start(0, 0);
-            continue;
-          }
-          wk[x].list = p.blocks != nullptr ? p.blocks + (static_cast<size_t>(bh) * p.GQ + g) * p.kb : nullptr;
-          const int n = p.blocks != nullptr ? wk[x].count(pw == 0) : min(p.nb, (len + p.BK - 1) / p.BK);
-          const int lo = static_cast<int>(static_cast<long long>(n) * sp / p.splits);
-          const int hi = static_cast<int>(static_cast<long long>(n) * (sp + 1) / p.splits);
-          wk[x].start(lo, hi - lo);
-          tn[x] = max(1, (hi - lo + BPS - 1) / BPS);
-        }
-        const int T = tn[0] + tn[1];
+        for (int x = 0; x < LISTS; ++x) u.tn[x] = open_list(wk[x], x, u.left[x]);
         if (!PAIR) {
-          tn[1] = T / 2;
-          tn[0] = T - tn[1];
+          u.tn[1] = u.tn[0] / 2;
+          u.tn[0] -= u.tn[1];
         }
-        const int2 tn2 = make_int2(tn[0], tn[1]);
-        const int both = 2 * min(tn[0], tn[1]), longer = tn[0] >= tn[1] ? 0 : 1;
-        if (pw == 0) {
-          // (the slot's unit is four back: the MMAs of the unit before this one are issued, so the
-          // epilogue of the one two before that has read its counts)
-          if (!mbar_wait_warp(q_empty, (u_it & 1) ^ 1, abort_flag, wl)) { okp = false; break; }
-          if (lane == 0) {
-            sUnit[u_it & 3] = tn2;
-            mbar_arrive(u_full + (u_it & 3));
-            mbar_arrive_expect_tx(q_full, L::TILE_BYTES);
+      }
+      return u;
+    };
+    // The blocks of the next stage of walk x: their number; this lane's entries off and off2 among them
+    // (meaningless from that number on).
+    auto take = [&](Unit& u, int x, int off, int off2, int& blk, int& blk2) {
+      auto from = [&](ListWalk& w, int& left) {
+        w.ensure(BPS);
+        const int n = min(min(BPS, left), w.have - w.at);
+        blk = __shfl_sync(0xffffffffu, w.cur, (w.at + off) & 31);
+        blk2 = __shfl_sync(0xffffffffu, w.cur, (w.at + off2) & 31);
+        w.at += n;
+        left -= n;
+        return n;
+      };
+      return PAIR && x ? from(wk[LISTS - 1], u.left[LISTS - 1]) : from(wk[0], u.left[0]);
+    };
+    uint32_t q_issued = 0;
+    // The unit's counts for the other roles (`only` >= 0: that stream's), and its Q tile (after the last
+    // QK^T of the one before).  The counts' slot was last the unit's four back: the MMAs of the unit
+    // before this one are issued, so the epilogue of the one two before that has read its own.
+    auto publish = [&](const Unit& u, int only) -> bool {
+      if (!mbar_wait_warp(q_empty, (u_it & 1) ^ 1, abort_flag, wl)) return false;
+      if (lane == 0) {
+        int2& slot = sUnit[u_it & 3];
+        if (only <= 0) slot.x = u.tn[0];
+        if (only != 0) slot.y = u.tn[1];
+        mbar_arrive(u_full + (u_it & 3));
+        if (only <= 0) {
+          mbar_arrive_expect_tx(q_full, L::TILE_BYTES);
 #pragma unroll
-            for (int h = 0; h < HD / 64; ++h)
-              tma_load_2d(sQ + h * HALF, &tmQ, h * 64, bh * p.Nq + ut * kTile, q_full);
-          }
-          ++q_issued;
-          __syncwarp();
+          for (int h = 0; h < HD / 64; ++h)
+            tma_load_2d(sQ + h * HALF, &tmQ, h * 64, u.bh * p.Nq + u.ut * kTile, q_full);
         }
-        if constexpr (!KV8) {
-          // ---- bf16 rows by TMA: warp 8 the keys, warp 9 the values, a box per block and 64 columns
-          for (int t = 0; t < T; ++t, ++kv_it) {
-            int blk[4] = {-1, -1, -1, -1};  // the stage's blocks (-1: none)
-            if (PAIR && (t < both ? (t & 1) : longer)) {
+      }
+      if (only <= 0) ++q_issued;
+      __syncwarp();
+      return true;
+    };
+    if constexpr (!KV8) {
+      // ---- bf16 rows by TMA, a box per block and 64 columns: warp 8 the keys, warp 9 the values; SUB:
+      // of stream A's list, warps 10 and 11 those of stream B's
+      if (SUB || pw < 2) {
+        constexpr int HB = HD / 64;
+        const bool keys = (pw & 1) == 0;
+        const int only = SUB ? pw >> 1 : -1;
+        const uint32_t ring = SUB ? KST / 2 : keys ? KST : VST;
+        const int slot0 = SUB ? (pw >> 1) * (KST / 2) : 0;  // this warp's ring in the slots
+        uint64_t* full = (keys ? k_full : v_full) + slot0;
+        uint64_t* empty = (keys ? k_empty : v_empty) + slot0;
+        uint64_t* fix = vfix + (SUB ? pw >> 1 : 0);
+        const uint32_t tiles = (keys ? sK : sV) + slot0 * L::TILE_BYTES;
+        const CUtensorMap* map = keys ? &tmK : &tmV;
+        // lane l copies columns 64 (l % HB) .. of block l / HB of a stage, and sizes up run l % 4
+        const int my_blk = lane / HB, my_col = lane % HB;
+        const int run_blk = (lane & 3) * 32 >> bk_log, run_off = ((lane & 3) * 32) & (p.BK - 1);
+        uint32_t n_fix = 0, issued = 0;
+        for (int unit = blockIdx.x; unit < p.num_units && okp; unit += gridDim.x, ++u_it) {
+          Unit u = open_unit(unit, only, keys);
+          if (keys && !publish(u, only)) { okp = false; break; }
+          const int T = u.tn[0] + u.tn[1], both = 2 * min(u.tn[0], u.tn[1]), longer = u.tn[0] >= u.tn[1] ? 0 : 1;
+          for (int t = 0; t < T; ++t) {
+            int blk, rb;
+            const int n = take(u, SUB ? 0 : t < both ? t & 1 : longer, my_blk, run_blk, blk, rb);  // blocks of this stage
+            const int valid = run_blk < n ? min(32, max(0, u.len - rb * p.BK - run_off)) : 0;
+            // a block reaches behind the last valid key
+            const bool cut = __any_sync(0xffffffffu, run_blk < n && valid < 32);
+            const uint32_t slot = issued % ring, ph = (issued / ring) & 1;
+            if (!mbar_wait_warp(empty + slot, ph ^ 1, abort_flag, wl)) { okp = false; break; }
+            const uint32_t dst = tiles + slot * L::TILE_BYTES;
+            // masked keys weigh 0, but 0 times whatever lies in their V rows need not be 0: rows of no
+            // block are cleared beside the copies, rows behind the last valid one after theirs
+            auto clear = [&](int r) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (i < BPS) blk[i] = wk[PAIR ? 1 : 0].next();
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (i < BPS) blk[i] = wk[0].next();
-            }
-            int loads = 0;
-            bool cut = false;  // a block reaches behind the last valid key
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              loads += blk[i] >= 0 ? 1 : 0;
-              cut |= blk[i] >= 0 && len - blk[i] * p.BK < p.BK;
-            }
-            // valid keys of run lane & 3 (32 keys, in block run * 32 / BK of the stage)
-            const int at = (lane & 3) * 32 >> bk_log;
-            const int mine = at == 0 ? blk[0] : at == 1 ? blk[1] : at == 2 ? blk[2] : blk[3];
-            const int valid = mine < 0 ? 0 : min(32, max(0, len - mine * p.BK - (((lane & 3) * 32) & (p.BK - 1))));
-            const uint32_t bytes = static_cast<uint32_t>(loads) << (bk_log + (HD == 128 ? 8 : 7));
-            auto copy = [&](uint32_t dst, const CUtensorMap* map, uint64_t* bar) {
-              if (lane == 0) {
-                mbar_arrive_expect_tx(bar, bytes);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (i < loads)
-#pragma unroll
-                    for (int h = 0; h < HD / 64; ++h)
-                      tma_load_2d(dst + h * HALF + i * p.BK * 128, map, h * 64, bkv * p.Nk + blk[i] * p.BK, bar);
-              }
-              __syncwarp();
+              for (int c = 0; c < HD / 8; ++c)
+                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst + sw128_offset(r, c, kTile)), "r"(0u)
+                             : "memory");
             };
-            if (pw == 0) {
-              const uint32_t ks = kv_it % KST;
-              if (!mbar_wait_warp(k_empty + ks, ((kv_it / KST) & 1) ^ 1, abort_flag, wl)) { okp = false; break; }
-              if (lane < 4) sInfo[ks].valid[lane] = valid;
+            if (keys) {
+              if (lane < 4) sInfo[slot0 + slot].valid[lane] = valid;
+            } else if (n < BPS) {
+              for (int r = n * p.BK + lane; r < kTile; r += 32) clear(r);
+              fence_proxy_async_smem();
+            }
+            const bool late = !keys && cut;
+            uint64_t* land = late ? fix : full + slot;
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(land, static_cast<uint32_t>(n * p.BK) * HD * 2);
+            __syncwarp();
+            if (my_blk < n)
+              tma_load_2d(dst + my_col * HALF + my_blk * p.BK * 128, map, my_col * 64, u.bkv * p.Nk + blk * p.BK, land);
+            __syncwarp();
+            if (late) {
+              mbar_drain(fix, n_fix & 1);
+              ++n_fix;
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (lane >= __shfl_sync(0xffffffffu, valid, r)) clear(r * 32 + lane);
+              fence_proxy_async_smem();
               __syncwarp();
-              copy(sK + ks * L::TILE_BYTES, &tmK, k_full + ks);
-            } else {
-              const uint32_t vs = kv_it % VST;
-              if (!mbar_wait_warp(v_empty + vs, ((kv_it / VST) & 1) ^ 1, abort_flag, wl)) { okp = false; break; }
-              const uint32_t dV = sV + vs * L::TILE_BYTES;
-              // masked keys weigh 0, but 0 times whatever lies in their V rows need not be 0: rows of no
-              // block are cleared beside the copies, rows behind the last valid one after theirs
-              auto clear = [&](int r) {
-#pragma unroll
-                for (int c = 0; c < HD / 8; ++c)
-                  asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dV + sw128_offset(r, c, kTile)), "r"(0u)
-                               : "memory");
-              };
-              if (loads < BPS) {
-                for (int r = loads * p.BK + lane; r < kTile; r += 32) clear(r);
-                fence_proxy_async_smem();
-                __syncwarp();
-              }
-              copy(dV, &tmV, cut ? vfix : v_full + vs);
-              if (cut) {
-                mbar_drain(vfix, n_fix & 1);
-                ++n_fix;
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                  if (lane >= __shfl_sync(0xffffffffu, valid, r)) clear(r * 32 + lane);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(v_full + vs);
-                __syncwarp();
-              }
+              if (lane == 0) mbar_arrive(full + slot);
+              __syncwarp();
             }
             ++issued;
           }
-        } else {
-          // ---- 8-bit rows: this warp's run of 32 keys of every stage
-          constexpr int LPR = HD / 16, RPI = 32 / LPR, NIT = 32 / RPI;
-          const int sub = lane / LPR, c = lane % LPR;
-          uint4 bk[NIT], bv[NIT];
-          float fks = 1.f, fvs = 1.f;
-          int valid = 0;
-          auto fetch = [&](int t) {
-            int mine = -1;
-            auto walk = [&](ListWalk& w) {
-              for (int i = 0; i < BPS; ++i) {
-                const int x = w.next();
-                if (pw * 32 >> bk_log == i) mine = x;
-              }
-            };
-            if (PAIR && (t < both ? (t & 1) : longer)) walk(wk[PAIR ? 1 : 0]);
-            else walk(wk[0]);
-            const int row0 = mine * p.BK + (pw * 32) % p.BK;
-            valid = mine < 0 ? 0 : min(32, max(0, len - row0));
-            fks = fvs = 1.f;
-            if (mine >= 0) {
-              fks = p.ks[static_cast<size_t>(bkv) * p.nb + mine];
-              fvs = p.vs[static_cast<size_t>(bkv) * p.nb + mine];
-            }
-            const size_t at = (static_cast<size_t>(bkv) * p.Nk + (mine < 0 ? 0 : row0)) * HD + c * 16;
-#pragma unroll
-            for (int it = 0; it < NIT; ++it) {
-              const int r = it * RPI + sub;
-              const bool in = r < valid;
-              bk[it] = in ? *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.K) + at + r * HD) : make_uint4(0u, 0u, 0u, 0u);
-            }
-#pragma unroll
-            for (int it = 0; it < NIT; ++it) {
-              const int r = it * RPI + sub;
-              const bool in = r < valid;
-              bv[it] = in ? *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.V) + at + r * HD) : make_uint4(0u, 0u, 0u, 0u);
-            }
-          };
-          // a lane's 16 values are two 16-byte chunks; every other lane stores its second one first,
-          // so that a store's eight lanes of a row group hit all eight bank groups
-          auto put = [&](uint32_t tile, const uint4* buf) {
-#pragma unroll
-            for (int it = 0; it < NIT; ++it) {
-              uint32_t w[8];
-              e4m3_to_bf16(buf[it], w);
-              const int r = pw * 32 + it * RPI + sub;
-              const bool swap = HD == 128 ? (c & 4) != 0 : (sub & 1) != 0;
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const bool second = (k == 1) != swap;
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(tile + sw128_offset(r, 2 * c + (second ? 1 : 0), kTile)),
-                             "r"(second ? w[4] : w[0]), "r"(second ? w[5] : w[1]), "r"(second ? w[6] : w[2]),
-                             "r"(second ? w[7] : w[3])
-                             : "memory");
-              }
-            }
-            fence_proxy_async_smem();
-          };
-          fetch(0);
-          for (int t = 0; t < T; ++t, ++kv_it) {
-            const uint32_t ks = kv_it % KST, vs = kv_it % VST;
-            if (!mbar_wait_warp(k_empty + ks, ((kv_it / KST) & 1) ^ 1, abort_flag, wl)) { okp = false; break; }
-            if (lane == 0) {
-              sInfo[ks].valid[pw] = valid;
-              sInfo[ks].ks[pw] = fks;
-              sInfo[ks].vs[pw] = fvs;
-            }
-            put(sK + ks * L::TILE_BYTES, bk);
-            mbar_arrive(k_full + ks);
-            if (!mbar_wait_warp(v_empty + vs, ((kv_it / VST) & 1) ^ 1, abort_flag, wl)) { okp = false; break; }
-            put(sV + vs * L::TILE_BYTES, bv);
-            mbar_arrive(v_full + vs);
-            if (t + 1 < T) fetch(t + 1);
-          }
         }
-      }
-      if (!okp) {
-        // after an abort, the TMA loads already issued land before the CTA releases its shared memory
-        // (on a normal exit every load has been consumed)
-        if (q_issued > 0) mbar_drain(q_full, (q_issued - 1) & 1);
-        if constexpr (!KV8) {
-          const uint32_t ring = pw == 0 ? KST : VST;
-          uint64_t* full = pw == 0 ? k_full : v_full;
+        if (!okp) {
+          // after an abort, the copies already issued land before the CTA releases its shared memory (on
+          // a normal exit every one has been consumed)
+          if (q_issued > 0) mbar_drain(q_full, (q_issued - 1) & 1);
           for (uint32_t s = 0; s < ring && s < issued; ++s) {
             const uint32_t last = issued - 1 - ((issued - 1 + ring - s) % ring);
             mbar_drain(full + s, (last / ring) & 1);
           }
         }
       }
+    } else {
+      // ---- 8-bit rows: every warp its run of 32 keys of each stage, widened to bf16 on the way
+      constexpr int LPR = HD / 16, RPI = 32 / LPR, NIT = 32 / RPI;
+      const int sub = lane / LPR, c = lane % LPR;
+      const int run_blk = pw * 32 >> bk_log, run_off = (pw * 32) & (p.BK - 1);
+      uint32_t it0 = 0, it1 = 0;  // stages so far (SUB: of stream A, of stream B)
+      for (int unit = blockIdx.x; unit < p.num_units && okp; unit += gridDim.x, ++u_it) {
+        Unit u = open_unit(unit, -1, pw == 0);
+        if (pw == 0 && !publish(u, -1)) { okp = false; break; }
+        const int T = u.tn[0] + u.tn[1], both = 2 * min(u.tn[0], u.tn[1]), longer = u.tn[0] >= u.tn[1] ? 0 : 1;
+        uint4 bk[NIT], bv[NIT];
+        float fks = 1.f, fvs = 1.f;
+        int valid = 0;
+        auto fetch = [&](int t) {
+          int blk, same;
+          if (take(u, t < both ? t & 1 : longer, run_blk, run_blk, blk, same) <= run_blk) blk = -1;
+          const int row0 = blk * p.BK + run_off;
+          valid = blk < 0 ? 0 : min(32, max(0, u.len - row0));
+          fks = fvs = 1.f;
+          if (blk >= 0) {
+            fks = p.ks[static_cast<size_t>(u.bkv) * p.nb + blk];
+            fvs = p.vs[static_cast<size_t>(u.bkv) * p.nb + blk];
+          }
+          const size_t at = (static_cast<size_t>(u.bkv) * p.Nk + (blk < 0 ? 0 : row0)) * HD + c * 16;
+#pragma unroll
+          for (int it = 0; it < NIT; ++it) {
+            const int r = it * RPI + sub;
+            bk[it] = r < valid ? *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.K) + at + r * HD) : make_uint4(0u, 0u, 0u, 0u);
+          }
+#pragma unroll
+          for (int it = 0; it < NIT; ++it) {
+            const int r = it * RPI + sub;
+            bv[it] = r < valid ? *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.V) + at + r * HD) : make_uint4(0u, 0u, 0u, 0u);
+          }
+        };
+        // a lane's 16 values are two 16-byte chunks; every other lane stores its second one first, so
+        // that a store's eight lanes of a row group hit all eight bank groups
+        auto put = [&](uint32_t tile, const uint4* buf) {
+#pragma unroll
+          for (int it = 0; it < NIT; ++it) {
+            uint32_t x[8];
+            e4m3_to_bf16(buf[it], x);
+            const int r = pw * 32 + it * RPI + sub;
+            const bool swap = HD == 128 ? (c & 4) != 0 : (sub & 1) != 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const bool second = (k == 1) != swap;
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(tile + sw128_offset(r, 2 * c + (second ? 1 : 0), kTile)),
+                           "r"(second ? x[4] : x[0]), "r"(second ? x[5] : x[1]), "r"(second ? x[6] : x[2]),
+                           "r"(second ? x[7] : x[3])
+                           : "memory");
+            }
+          }
+          fence_proxy_async_smem();
+        };
+        fetch(0);
+        for (int t = 0; t < T; ++t) {
+          uint32_t ks, vs, kph, vph;
+          if (SUB) {
+            const int x = t < both ? t & 1 : longer;
+            const uint32_t it = x ? it1++ : it0++;
+            ks = vs = x * (KST / 2) + it % (KST / 2);
+            kph = vph = (it / (KST / 2)) & 1;
+          } else {
+            ks = it0 % KST, kph = (it0 / KST) & 1;
+            vs = it0 % VST, vph = (it0 / VST) & 1;
+            ++it0;
+          }
+          if (!mbar_wait_warp(k_empty + ks, kph ^ 1, abort_flag, wl)) { okp = false; break; }
+          if (lane == 0) {
+            sInfo[ks].valid[pw] = valid;
+            sInfo[ks].ks[pw] = fks;
+            sInfo[ks].vs[pw] = fvs;
+          }
+          put(sK + ks * L::TILE_BYTES, bk);
+          mbar_arrive(k_full + ks);
+          if (!mbar_wait_warp(v_empty + vs, vph ^ 1, abort_flag, wl)) { okp = false; break; }
+          put(sV + vs * L::TILE_BYTES, bv);
+          mbar_arrive(v_full + vs);
+          if (t + 1 < T) fetch(t + 1);
+        }
+      }
+      if (!okp && pw == 0 && q_issued > 0) mbar_drain(q_full, (q_issued - 1) & 1);
     }
   } else if (warp >= 12) {
     // ------------------------------------------------------------------ MMA issuer
@@ -579,7 +622,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const uint64_t dK0 = desc_sw128(sK, 16, 1024);
       const uint64_t dV0 = desc_sw128(sV, HALF, 1024);
       constexpr uint64_t kSlotStep = L::TILE_BYTES >> 4;
-      uint32_t kv_base = 0, u_it = 0;
+      uint32_t u_it = 0;
       bool ok = true;
       if (p.hold != nullptr) {
         if (lane == 0) {
@@ -595,18 +638,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
-      auto wait_k = [&](int t) -> bool {
-        const uint32_t it = kv_base + t;
-        return mbar_wait_warp(k_full + it % KST, (it / KST) & 1, abort_flag, wl);
+      auto wait_at = [&](uint64_t* full, uint32_t it, uint32_t ring) -> bool {  // stage `it` of a ring
+        return mbar_wait_warp(full + it % ring, (it / ring) & 1, abort_flag, wl);
       };
-      auto wait_v = [&](int t) -> bool {
-        const uint32_t it = kv_base + t;
-        return mbar_wait_warp(v_full + it % VST, (it / VST) & 1, abort_flag, wl);
-      };
-      // S_x of the stage at place t (SUB: of its half h)
-      auto qk_mmas = [&](int t, int x, int h) {
-        const uint32_t ks = (kv_base + t) % KST;
-        const uint64_t dK = dK0 + ks * kSlotStep + h * (64 * 128 >> 4);
+      // S_x of the keys in a slot (SUB: of their half h)
+      auto qk_mmas = [&](uint32_t slot, int x, int h) {
+        const uint64_t dK = dK0 + slot * kSlotStep + h * (64 * 128 >> 4);
         const uint32_t dS = tmem + kTmS + x * kTile + h * 64;
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
@@ -615,88 +652,83 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         mma_commit_warp((h ? s_hi : s_full) + x);
       };
-      // k steps [from, to) of O += P V for the stage at place t
-      auto pv_mmas = [&](int t, int x, int h, int from, int to, bool first) {
-        const uint64_t dV = dV0 + ((kv_base + t) % VST) * kSlotStep + h * (4 * 2048 >> 4);
+      // k steps [from, to) of O += P V for the values in a slot (SUB: their half h)
+      auto pv_mmas = [&](uint32_t slot, int x, int h, int from, int to, bool first) {
+        const uint64_t dV = dV0 + slot * kSlotStep + h * (4 * 2048 >> 4);
         const uint32_t tO = tmem + kTmO + (SUB ? 2 * x + h : x) * HD, tP = tmem + kTmS + x * kTile + h * 64;
 #pragma unroll
         for (int kk = from; kk < to; ++kk)
           mma_bf16_ts_warp(tO, tP + kk * 8, dV + kk * (2048 >> 4), IDESC_PV, (!first || kk > 0) ? 1u : 0u);
       };
-      if constexpr (PAIR) {
-        // one warp for each stream (SUB: and half of its keys), which waits for nothing of the others
+      if constexpr (SUB) {
+        // One warp for each stream and half of its keys, which waits for nothing of the others: the
+        // streams have a ring each (a shared one's phases could pass a waiting warp by).
+        constexpr uint32_t RING = KST / 2;
         const int x = (warp - 12) & 1, h = (warp - 12) >> 1;
-        uint32_t sc = 0;  // PVs issued (barrier phases)
+        const uint32_t s0 = x * RING;
+        uint32_t sc = 0;  // stages done (ring places and barrier phases)
         for (int unit = blockIdx.x; unit < p.num_units && ok; unit += gridDim.x, ++u_it) {
           ok = mbar_wait_warp(u_full + (u_it & 3), (u_it >> 2) & 1, abort_flag, wl);
           if (!ok) break;
-          const int2 tn = sUnit[u_it & 3];
-          const int Tx = x ? tn.y : tn.x;
-          ok = mbar_wait_warp(q_full, u_it & 1, abort_flag, wl) && (Tx == 0 || wait_k(stage_pos(tn, x, 0)));
+          const int Tx = x ? sUnit[u_it & 3].y : sUnit[u_it & 3].x;
+          ok = mbar_wait_warp(q_full, u_it & 1, abort_flag, wl) && (Tx == 0 || wait_at(k_full + s0, sc, RING));
           if (!ok) break;
-          if (Tx > 0) qk_mmas(stage_pos(tn, x, 0), x, h);
+          if (Tx > 0) qk_mmas(s0 + sc % RING, x, h);
           if (Tx <= 1) mma_commit_warp(q_empty);
+          if (Tx == 0) ok = mbar_wait_warp(o_empty, (u_it & 1) ^ 1, abort_flag, wl);  // keep step with its phases
           for (int i = 0; i < Tx; ++i, ++sc) {
-            const int t = stage_pos(tn, x, i);
             const bool next = i + 1 < Tx;
-            const int tnext = next ? stage_pos(tn, x, i + 1) : 0;
-            ok = (!next || wait_k(tnext)) && wait_v(t) &&
+            ok = (!next || wait_at(k_full + s0, sc + 1, RING)) && wait_at(v_full + s0, sc, RING) &&
                  (i != 0 || mbar_wait_warp(o_empty, (u_it & 1) ^ 1, abort_flag, wl)) &&
-                 mbar_wait_warp((SUB && h == 1 ? p_full : p_half) + x, sc & 1, abort_flag, wl);
+                 mbar_wait_warp((h ? p_full : p_half) + x, sc & 1, abort_flag, wl);
             if (!ok) break;
             tc_fence_after();  // P_x was written by tcgen05.st of the softmax
-            if constexpr (SUB) {
-              pv_mmas(t, x, h, 0, 4, i == 0);
-              mma_commit_warp((h ? pv_done : pvlo_done) + x);
-            } else {
-              pv_mmas(t, x, 0, 0, 2 * kPSplit, i == 0);
-              mma_commit_warp(pvlo_done + x);
-              ok = mbar_wait_warp(p_full + x, sc & 1, abort_flag, wl);
-              if (!ok) break;
-              tc_fence_after();
-              pv_mmas(t, x, 0, 2 * kPSplit, kTile / 16, false);
-              mma_commit_warp(pv_done + x);
-            }
-            mma_commit_warp(v_empty + (kv_base + t) % VST);
+            pv_mmas(s0 + sc % RING, x, h, 0, 4, i == 0);
+            mma_commit_warp((h ? pv_done : pvlo_done) + x);
+            mma_commit_warp(v_empty + s0 + sc % RING);
             if (next) {
-              qk_mmas(tnext, x, h);
+              qk_mmas(s0 + (sc + 1) % RING, x, h);
               if (i + 2 == Tx) mma_commit_warp(q_empty);
             }
           }
-          kv_base += tn.x + tn.y;
         }
       } else {
-        uint32_t sc0 = 0, sc1 = 0;  // PVs issued per stream (barrier phases)
+        uint32_t kv_base = 0, sc0 = 0, sc1 = 0;  // stages of earlier units; PVs issued per stream (barrier phases)
         for (int unit = blockIdx.x; unit < p.num_units && ok; unit += gridDim.x, ++u_it) {
           ok = mbar_wait_warp(u_full + (u_it & 3), (u_it >> 2) & 1, abort_flag, wl);
           if (!ok) break;
           const int2 tn = sUnit[u_it & 3];
-          const int T = tn.x + tn.y;  // stages alternate between the streams
-          ok = mbar_wait_warp(q_full, u_it & 1, abort_flag, wl) && wait_k(0) && (T < 2 || wait_k(1));
+          const int T = tn.x + tn.y, both = 2 * min(tn.x, tn.y), longer = tn.x >= tn.y ? 0 : 1;
+          ok = mbar_wait_warp(q_full, u_it & 1, abort_flag, wl) && wait_at(k_full, kv_base, KST) &&
+               (both == 0 || wait_at(k_full, kv_base + 1, KST));
           if (!ok) break;
-          qk_mmas(0, 0, 0);
-          if (T > 1) qk_mmas(1, 1, 0);
-          if (T <= 2) mma_commit_warp(q_empty);
+          qk_mmas(kv_base % KST, 0, 0);
+          if (both > 0) qk_mmas((kv_base + 1) % KST, 1, 0);
+          if (T == max(both, 1) && T <= 2) mma_commit_warp(q_empty);
+          int n0 = 0, n1 = 0;  // stages of each stream done in this unit
           for (int t = 0; t < T && ok; ++t) {
-            const int x = t & 1;
-            const bool next = t + 2 < T;
-            ok = mbar_wait_warp(p_half + x, (x ? sc1 : sc0) & 1, abort_flag, wl) && wait_v(t) &&
+            const int x = PAIR && t >= both ? longer : t & 1;
+            const int mine = PAIR ? (x ? n1 : n0) : t >> 1;
+            const bool next = PAIR ? mine + 1 < (x ? tn.y : tn.x) : t + 2 < T;
+            const int tnext = PAIR ? stage_pos(tn, x, mine + 1) : t + 2;
+            ok = mbar_wait_warp(p_half + x, (x ? sc1 : sc0) & 1, abort_flag, wl) && wait_at(v_full, kv_base + t, VST) &&
                  (t != 0 || mbar_wait_warp(o_empty, (u_it & 1) ^ 1, abort_flag, wl));
             if (!ok) break;
             tc_fence_after();  // P_x was written by tcgen05.st of the softmax
-            pv_mmas(t, x, 0, 0, 2 * kPSplit, t < 2);
+            pv_mmas((kv_base + t) % VST, x, 0, 0, 2 * kPSplit, mine == 0);
             mma_commit_warp(pvlo_done + x);
-            ok = mbar_wait_warp(p_full + x, (x ? sc1 : sc0) & 1, abort_flag, wl) && (!next || wait_k(t + 2));
+            ok = mbar_wait_warp(p_full + x, (x ? sc1 : sc0) & 1, abort_flag, wl) &&
+                 (!next || wait_at(k_full, kv_base + tnext, KST));
             if (!ok) break;
             tc_fence_after();
-            pv_mmas(t, x, 0, 2 * kPSplit, kTile / 16, false);
+            pv_mmas((kv_base + t) % VST, x, 0, 2 * kPSplit, kTile / 16, false);
             mma_commit_warp(pv_done + x);
             mma_commit_warp(v_empty + (kv_base + t) % VST);
-            if (x) ++sc1;
-            else ++sc0;
+            if (x) ++sc1, ++n1;
+            else ++sc0, ++n0;
             if (next) {
-              qk_mmas(t + 2, x, 0);
-              if (t + 3 == T) mma_commit_warp(q_empty);
+              qk_mmas((kv_base + tnext) % KST, x, 0);
+              if (tnext == T - 1) mma_commit_warp(q_empty);
             }
           }
           kv_base += T;
@@ -734,7 +766,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         float m_pend = -INFINITY;  // a raise of the reference decided by the stream's previous stage
         for (int i = 0; i < Tx; ++i, ++sc) {
           if (!mbar_wait_warp(s_mine, sc & 1, abort_flag, wl)) { ok = false; break; }
-          const uint32_t slot = (kv_base + stage_pos(tn, x, i)) % KST;
+          const uint32_t slot = SUB ? x * (KST / 2) + sc % (KST / 2) : (kv_base + stage_pos(tn, x, i)) % KST;
           int vq[RUNS], all = 32;
           float kq[RUNS], vsq[RUNS];
 #pragma unroll

@@ -231,6 +231,9 @@ SHAPES = [
     (1, 1, 1, 1, 1, 128, 1, 32, 1, None, None, False),
     (1, 1, 1, 40, 9000, 128, 64, 64, 130, "any", None, False),
     (1, 1, 1, 2, 9000, 64, 1, 32, 250, "sorted", [8999], True),
+    (1, 3, 3, 1000, 8192, 64, 64, 64, 100, "holes", None, False),  # many stages, lists of unlike lengths
+    (1, 3, 1, 1000, 8192, 128, 64, 32, 200, "holes", [8000], False),
+    (2, 2, 2, 1100, 6000, 128, 128, 64, 60, "holes", [6000, 100], False),
 ]
 
 
