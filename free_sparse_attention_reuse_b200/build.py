@@ -12,7 +12,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmcs.so")
 SOURCES = ["mcs_api.cu"]
 DEPS = ["mcs_api.cu", "sm100.cuh", "attn.cuh", "select.cuh", "pddp.cuh", "variants.cuh", "kmeans.cuh",
-        "rotary.cuh", "blocks.cuh", "block_attn.cuh", "block_api.cuh"]
+        "rotary.cuh", "blocks.cuh", "block_attn.cuh", "block_token.cuh", "block_api.cuh"]
 HEADER = os.path.join(os.path.dirname(HERE), "include", "mcs.h")
 
 

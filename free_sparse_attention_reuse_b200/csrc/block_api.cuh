@@ -4,6 +4,7 @@
 #pragma once
 
 #include "block_attn.cuh"
+#include "block_token.cuh"
 
 namespace {
 
@@ -53,13 +54,14 @@ mcs_status block_device(DeviceInfo** out) {
 // launch agree.  Without lists every query head of a key/value head attends to the same keys: their
 // rows, which lie one behind the other, count as one head's.
 struct BlockPlan {
-  bool tensor;       // the tcgen05 kernel (else one warp per row)
+  bool tensor;       // the tcgen05 kernel (else the one for few rows)
   bool pair;         // lists of 64 rows: two to a tile
   int H, Nq, C, GQ;  // as the kernel sees them
   int tiles, splits;
   size_t part, total;  // workspace: bytes of the parts' results, and all
 };
 constexpr int kPlanSms = 148;
+constexpr long long kTokenCtas = 888;
 
 BlockPlan plan_block_attn(const mcs_block_shape& s, int C, int BK, int kb, bool listed) {
   BlockPlan q{};
@@ -68,26 +70,52 @@ BlockPlan plan_block_attn(const mcs_block_shape& s, int C, int BK, int kb, bool 
   q.C = C;
   q.tensor = listed ? C >= 64 : q.Nq > 16;
   q.pair = q.tensor && listed && C == 64;
-  q.GQ = (q.Nq + C - 1) / C;
+  if (!listed && !q.tensor) q.C = 16;
+  q.GQ = (q.Nq + q.C - 1) / q.C;
   q.tiles = (q.Nq + kTile - 1) / kTile;
   q.splits = 1;
+  const long long lists = static_cast<long long>(s.B) * q.H * (q.tensor ? q.tiles : q.GQ);
   if (q.tensor) {
     if (!q.pair) q.GQ = q.tiles;
     // Few tiles: the keys of a tile are split over several CTAs.  The cost of a choice, in stages of
     // 128 keys: waves times (the part's stages and about three of start and end), and six for the
     // join's launch.
-    const long long units = static_cast<long long>(s.B) * q.H * q.tiles;
     const int T = static_cast<int>((static_cast<long long>(kb) * BK + kTile - 1) / kTile);
     long long best = -1;
     for (int n = 1; n <= 32 && (n == 1 || T / n >= 4); ++n) {
-      const long long cost = (units * n + kPlanSms - 1) / kPlanSms * ((T + n - 1) / n + 3) + (n > 1 ? 6 : 0);
+      const long long cost = (lists * n + kPlanSms - 1) / kPlanSms * ((T + n - 1) / n + 3) + (n > 1 ? 6 : 0);
       if (best < 0 || cost < best) best = cost, q.splits = n;
     }
+  } else {
+    // enough CTAs to fill the GPU some times over, each with at least 256 keys
+    const long long keys = static_cast<long long>(kb) * BK;
+    q.splits = static_cast<int>(std::max(1ll, std::min(std::min((kTokenCtas + lists - 1) / lists, keys / 256), 128ll)));
   }
   const size_t rows = static_cast<size_t>(s.B) * s.H * s.Nq;
   if (q.splits > 1) q.part = round_up(rows * q.splits * s.d * 4, 256);
   q.total = q.part + (q.splits > 1 ? round_up(rows * q.splits * 4, 256) : 256);
   return q;
+}
+
+// Parts of split lists, joined behind the kernel that wrote them.
+template <int HD>
+void join_parts(const BlockAttnParams& p, cudaStream_t st) {
+  if (p.splits == 1) return;
+  const long long rows = static_cast<long long>(p.B) * p.H * p.Nq;
+  constexpr int per = 256 / (HD / 4);
+  block_join_kernel<HD><<<static_cast<unsigned>((rows + per - 1) / per), 256, 0, st>>>(p);
+}
+
+template <int HD>
+mcs_status run_block_token(const BlockAttnParams& p, bool kv8, cudaStream_t st) {
+  const unsigned grid = static_cast<unsigned>(static_cast<long long>(p.B) * p.H * p.GQ * p.splits);
+  const bool few = std::min(p.C, p.Nq) <= 8;
+  if (kv8 && few) block_token_kernel<HD, true, 8><<<grid, kTokenWarps * 32, 0, st>>>(p);
+  else if (kv8) block_token_kernel<HD, true, 16><<<grid, kTokenWarps * 32, 0, st>>>(p);
+  else if (few) block_token_kernel<HD, false, 8><<<grid, kTokenWarps * 32, 0, st>>>(p);
+  else block_token_kernel<HD, false, 16><<<grid, kTokenWarps * 32, 0, st>>>(p);
+  join_parts<HD>(p, st);
+  return launch_status();
 }
 
 template <int HD, bool KV8, bool PAIR>
@@ -101,11 +129,7 @@ mcs_status run_block_attn(const BlockAttnParams& p, cudaStream_t st, int sms) {
     if (!make_row_map(&tmK, p.K, rows, HD, p.BK) || !make_row_map(&tmV, p.V, rows, HD, p.BK)) return MCS_ERR_CUDA;
   }
   block_attn_kernel<HD, KV8, PAIR><<<std::min(p.num_units, sms), kAttnThreads, BlockSmem<HD>::BYTES, st>>>(tmQ, tmK, tmV, p);
-  if (p.splits > 1) {
-    const long long rows = static_cast<long long>(p.B) * p.H * p.Nq;
-    constexpr int per = 256 / (HD / 4);
-    block_join_kernel<HD><<<static_cast<unsigned>((rows + per - 1) / per), 256, 0, st>>>(p);
-  }
+  join_parts<HD>(p, st);
   return launch_status();
 }
 template <int HD>
@@ -366,16 +390,7 @@ mcs_status mcs_block_attn(mcs_block_shape s, const void* Q, const void* K, const
   if (plan.tensor)
     return s.d == 64 ? run_block_attn<64>(p, kv_format != 0, plan.pair, st, di->sms)
                      : run_block_attn<128>(p, kv_format != 0, plan.pair, st, di->sms);
-  const long long rows = static_cast<long long>(s.B) * s.H * s.Nq;
-  const unsigned grid = static_cast<unsigned>((rows + kSimpleWarps - 1) / kSimpleWarps);
-  if (s.d == 64) {
-    if (kv_format) block_attn_simple_kernel<64, true><<<grid, kSimpleWarps * 32, 0, st>>>(p);
-    else block_attn_simple_kernel<64, false><<<grid, kSimpleWarps * 32, 0, st>>>(p);
-  } else {
-    if (kv_format) block_attn_simple_kernel<128, true><<<grid, kSimpleWarps * 32, 0, st>>>(p);
-    else block_attn_simple_kernel<128, false><<<grid, kSimpleWarps * 32, 0, st>>>(p);
-  }
-  return launch_status();
+  return s.d == 64 ? run_block_token<64>(p, kv_format != 0, st) : run_block_token<128>(p, kv_format != 0, st);
 }
 
 }  // extern "C"
