@@ -351,6 +351,47 @@ E4M3 = torch.float8_e4m3fn
 BLOCK_ROWS = (32, 64, 128)      # keys of a block
 QUERY_ROWS = (1, 16, 64, 128)   # query rows that share a list
 
+# Calls that passed every check, by what the checks look at (types, shapes, strides, devices and plain
+# arguments; never an address): what the call needs beside its pointers.  These calls take as little as
+# ten microseconds on the device, so a repeated one does not check the same shapes again.
+_plans: dict = {}
+
+
+def _key(name, tensors, *rest):
+    """Hashable account of a call, or None for one that the checks have to look at."""
+    try:
+        k = (name, rest, tuple([None if t is None else (t.dtype, t.shape, t.stride(), t.device) for t in tensors]))
+        hash(k)
+        return k
+    except (AttributeError, TypeError):
+        return None
+
+
+def _keep(key, plan):
+    if key is not None:
+        if len(_plans) >= 512:
+            _plans.clear()
+        _plans[key] = plan
+    return plan
+
+
+def _here(device):
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device} but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _workspace(ws, n: int, device):
+    if ws is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    _spec(ws, "ws", torch.uint8)
+    if ws.device != device:
+        raise ValueError(f"ws is on {ws.device}, other arguments on {device}")
+    return ws
+
 
 def _heads(t, name: str, dtype=torch.bfloat16):
     if not isinstance(t, torch.Tensor) or t.dim() != 4:
@@ -377,7 +418,8 @@ def _strides(t):
 
 
 def _apart(outs: dict, ins: dict):
-    """No output may share memory with an input: the kernels read inputs after they have written."""
+    """No output that the caller gives may share memory with an input: inputs are read after outputs
+    have been written."""
     def span(t):
         n = 1 + sum((s - 1) * st for s, st in zip(t.shape, t.stride())) if t.numel() else 0
         return t.data_ptr(), t.data_ptr() + n * t.element_size()
@@ -396,19 +438,7 @@ def _length(t, name: str, B: int):
         _spec(t, name, torch.int32, (B,))
 
 
-def rotary(q, k, v, pos, axes, theta: float = 10000.0, pairs: str = "adjacent", norm=None, q_weight=None,
-           k_weight=None, eps: float = 1e-6, out=None):
-    """A layer's projections to attention-ready tensors in one pass: RMS norm of q and k, rotary
-    positions over several axes, and the change to head-major layout.
-
-    q [B, N, H, d], k and v [B, N, Hkv, d]: bf16 views (for example the parts of a fused projection
-    [B, N, 3, H, d]) with consecutive elements in a row; k and v may be None.  pos: int32 or fp32
-    [N, A] or [B, N, A], a token's position on each of the A axes.  axes: how many of a row's d
-    elements each axis turns (even; elements behind their sum stay).  theta: base of the
-    frequencies.  pairs: "adjacent" (elements 2i, 2i+1) or "halves" (i, i + sum(axes)/2).  norm:
-    None, "head" (over a row, weights [d]) or "token" (over all heads of a token, weights
-    [heads, d]); weights fp32 or bf16, or None for ones.  Returns Q [B, H, N, d], K and V
-    [B, Hkv, N, d] contiguous (None where the input is None); out = (Q, K, V) to reuse buffers."""
+def _plan_rotary(q, k, v, pos, axes, theta, pairs, norm, q_weight, k_weight, eps, out):
     if pairs not in ("adjacent", "halves"):
         raise ValueError(f"pairs must be 'adjacent' or 'halves', got {pairs!r}")
     if norm not in (None, "head", "token"):
@@ -454,17 +484,15 @@ def rotary(q, k, v, pos, axes, theta: float = 10000.0, pairs: str = "adjacent", 
             raise ValueError("q_weight and k_weight must have one dtype")
         wdt = w.dtype
         _spec(w, name, wdt, (d,) if norm == "head" else (heads, d))
-    if out is None:
-        mk = lambda h: torch.empty((B, h, N, d), dtype=torch.bfloat16, device=q.device)  # noqa: E731
-        out = (mk(H), None if k is None else mk(Hkv), None if v is None else mk(Hkv))
-    Q, K, V = out
-    for t, o, name, heads in ((q, Q, "Q", H), (k, K, "K", Hkv), (v, V, "V", Hkv)):
-        if (t is None) != (o is None):
-            raise ValueError(f"{name} must be given exactly where its input is")
-        if o is not None:
-            _spec(o, name, torch.bfloat16, (B, heads, N, d))
-    _on_device(q=q, k=k, v=v, pos=pos, q_weight=q_weight, k_weight=k_weight, Q=Q, K=K, V=V)
-    _apart(dict(Q=Q, K=K, V=V), dict(q=q, k=k, v=v))
+    shapes = [(B, H, N, d), None if k is None else (B, Hkv, N, d), None if v is None else (B, Hkv, N, d)]
+    if out is not None:
+        for o, shape, name in zip(out, shapes, ("Q", "K", "V")):
+            if (o is None) != (shape is None):
+                raise ValueError(f"{name} must be given exactly where its input is")
+            if o is not None:
+                _spec(o, name, torch.bfloat16, shape)
+    _on_device(q=q, k=k, v=v, pos=pos, q_weight=q_weight, k_weight=k_weight,
+               **({} if out is None else dict(Q=out[0], K=out[1], V=out[2])))
     a = _lib.RotaryArgs(B=B, N=N, H=H, Hkv=Hkv, d=d, axes=len(axes), theta=theta, eps=eps,
                         pairs=int(pairs == "halves"), norm=(None, "head", "token").index(norm),
                         pos_is_float=int(pos.dtype == torch.float32), pos_per_batch=int(pos.dim() == 3),
@@ -474,34 +502,66 @@ def rotary(q, k, v, pos, axes, theta: float = 10000.0, pairs: str = "adjacent", 
     for i, t in enumerate((q, k, v)):
         if t is not None:
             a.stride[i][:] = _strides(t)
-    check(_lib.load().mcs_rotary(a, ptr(q), ptr(k), ptr(v), ptr(pos), ptr(q_weight), ptr(k_weight), ptr(Q), ptr(K),
-                                 ptr(V), stream_ptr()), "mcs_rotary")
+    return a, shapes
+
+
+def rotary(q, k, v, pos, axes, theta: float = 10000.0, pairs: str = "adjacent", norm=None, q_weight=None,
+           k_weight=None, eps: float = 1e-6, out=None):
+    """A layer's projections to attention-ready tensors in one pass: RMS norm of q and k, rotary
+    positions over several axes, and the change to head-major layout.
+
+    q [B, N, H, d], k and v [B, N, Hkv, d]: bf16 views (for example the parts of a fused projection
+    [B, N, 3, H, d]) with consecutive elements in a row; k and v may be None.  pos: int32 or fp32
+    [N, A] or [B, N, A], a token's position on each of the A axes.  axes: how many of a row's d
+    elements each axis turns (even; elements behind their sum stay).  theta: base of the
+    frequencies.  pairs: "adjacent" (elements 2i, 2i+1) or "halves" (i, i + sum(axes)/2).  norm:
+    None, "head" (over a row, weights [d]) or "token" (over all heads of a token, weights
+    [heads, d]); weights fp32 or bf16, or None for ones.  Returns Q [B, H, N, d], K and V
+    [B, Hkv, N, d] contiguous (None where the input is None); out = (Q, K, V) to reuse buffers."""
+    key = _key("rotary", (q, k, v, pos, q_weight, k_weight, *(out or ())), axes if type(axes) is tuple else None, theta,
+               pairs, norm, eps) if type(axes) is tuple else None
+    plan = _plans.get(key) if key is not None else None
+    if plan is None:
+        plan = _keep(key, _plan_rotary(q, k, v, pos, axes, theta, pairs, norm, q_weight, k_weight, eps, out))
+    a, shapes = plan
+    dev = q.device
+    _here(dev)
+    if out is None:
+        out = tuple([None if s is None else torch.empty(s, dtype=torch.bfloat16, device=dev) for s in shapes])
+    else:
+        _apart(dict(Q=out[0], K=out[1], V=out[2]), dict(q=q, k=k, v=v, pos=pos, q_weight=q_weight, k_weight=k_weight))
+    Q, K, V = out
+    check(_lib.load().mcs_rotary(a, _at(q), _at(k), _at(v), _at(pos), _at(q_weight), _at(k_weight), _at(Q), _at(K),
+                                 _at(V), stream_ptr()), "mcs_rotary")
     return Q, K, V
+
+
+def _plan_means(K, BK, kv_len, means):
+    B, H, N, d = _heads(K, "K")
+    _block_sizes(BK=BK)
+    _length(kv_len, "kv_len", B)
+    shape = (B, H, -(-N // BK), d)
+    if means is not None:
+        _spec(means, "means", torch.float32, shape)
+    _on_device(K=K, kv_len=kv_len, means=means)
+    return Shape(B, H, N, d, 0.0), shape
 
 
 def block_means(K, BK: int, kv_len=None, means=None):
     """Mean of the valid rows of every block of BK rows: fp32 [B, H, ceil(N / BK), d] (zero for a
     block without one).  kv_len: int32 [B], valid rows of each batch entry."""
-    B, H, N, d = _heads(K, "K")
-    _block_sizes(BK=BK)
-    _length(kv_len, "kv_len", B)
-    shape = (B, H, -(-N // BK), d)
+    key = _key("means", (K, kv_len, means), BK)
+    s, shape = _plans.get(key) or _keep(key, _plan_means(K, BK, kv_len, means))
+    _here(K.device)
     if means is None:
         means = torch.empty(shape, dtype=torch.float32, device=K.device)
-    _spec(means, "means", torch.float32, shape)
-    _on_device(K=K, kv_len=kv_len, means=means)
-    check(_lib.load().mcs_block_means(Shape(B, H, N, d, 0.0), ptr(K), BK, ptr(kv_len), ptr(means), stream_ptr()),
-          "mcs_block_means")
+    else:
+        _apart(dict(means=means), dict(K=K, kv_len=kv_len))
+    check(_lib.load().mcs_block_means(s, _at(K), BK, _at(kv_len), _at(means), stream_ptr()), "mcs_block_means")
     return means
 
 
-def block_topk(Q, means, C: int, kb: int, BK: int, kv_len=None, blocks=None, ws=None):
-    """The kb key blocks of largest pooled score for every block of C query rows: int32
-    [B, H, ceil(Nq / C), kb], ascending, -1 behind them where fewer blocks hold a valid key.
-
-    means: fp32 [B, Hkv, nb, d] from block_means or cache_write.  score = (mean of the query rows) .
-    (mean of the block's keys), ties to the lower block.  kv_len: int32 [B], valid keys; a block
-    behind them is not a candidate."""
+def _plan_topk(Q, means, C, kb, BK, kv_len, blocks):
     B, H, Nq, d = _heads(Q, "Q")
     Hkv, nb = _heads(means, "means", torch.float32)[1:3]
     _spec(means, "means", torch.float32, (B, Hkv, nb, d))
@@ -511,33 +571,38 @@ def block_topk(Q, means, C: int, kb: int, BK: int, kv_len=None, blocks=None, ws=
         raise ValueError(f"kb must be in [1, {nb}], got {kb}")
     _length(kv_len, "kv_len", B)
     shape = (B, H, -(-Nq // C), kb)
-    if blocks is None:
-        blocks = torch.empty(shape, dtype=torch.int32, device=Q.device)
-    _spec(blocks, "blocks", torch.int32, shape)
+    if blocks is not None:
+        _spec(blocks, "blocks", torch.int32, shape)
     _on_device(Q=Q, means=means, kv_len=kv_len, blocks=blocks)
-    lib = _lib.load()
     s = _lib.BlockShape(B, H, Hkv, Nq, nb * BK, d, 0.0)
-    if ws is None:
-        n = int(lib.mcs_block_topk_workspace_size(s, C, BK))
-        if n == 0:
-            raise _lib.MCSError(2, "mcs_block_topk_workspace_size: invalid shape")
-        ws = torch.empty(n, dtype=torch.uint8, device=Q.device)
-    _spec(ws, "ws", torch.uint8)
-    _on_device(Q=Q, ws=ws)
-    check(lib.mcs_block_topk(s, ptr(Q), ptr(means), C, BK, kb, ptr(kv_len), ptr(blocks), ptr(ws), ws.numel(),
-                             stream_ptr()), "mcs_block_topk")
+    n = int(_lib.load().mcs_block_topk_workspace_size(s, C, BK))
+    if n == 0:
+        raise _lib.MCSError(2, "mcs_block_topk_workspace_size: invalid shape")
+    return s, shape, n
+
+
+def block_topk(Q, means, C: int, kb: int, BK: int, kv_len=None, blocks=None, ws=None):
+    """The kb key blocks of largest pooled score for every block of C query rows: int32
+    [B, H, ceil(Nq / C), kb], ascending, -1 behind them where fewer blocks hold a valid key.
+
+    means: fp32 [B, Hkv, nb, d] from block_means or cache_write.  score = (mean of the query rows) .
+    (mean of the block's keys), ties to the lower block.  kv_len: int32 [B], valid keys; a block
+    behind them is not a candidate."""
+    key = _key("topk", (Q, means, kv_len, blocks), C, kb, BK)
+    s, shape, n = _plans.get(key) or _keep(key, _plan_topk(Q, means, C, kb, BK, kv_len, blocks))
+    dev = Q.device
+    _here(dev)
+    if blocks is None:
+        blocks = torch.empty(shape, dtype=torch.int32, device=dev)
+    else:
+        _apart(dict(blocks=blocks), dict(Q=Q, means=means, kv_len=kv_len))
+    ws = _workspace(ws, n, dev)
+    check(_lib.load().mcs_block_topk(s, _at(Q), _at(means), C, BK, kb, _at(kv_len), _at(blocks), _at(ws), ws.numel(),
+                                     stream_ptr()), "mcs_block_topk")
     return blocks
 
 
-def block_attn(Q, K, V, blocks, C: int, BK: int, R=None, kv_len=None, k_scale=None, v_scale=None, out=None, lse=None,
-               want_lse: bool = False, ws=None, scale=None):
-    """Attention over the key blocks that each block of C query rows lists; returns (out, lse), lse
-    None unless wanted.
-
-    Q [B, H, Nq, d] bf16; K, V [B, Hkv, Nk, d] bf16, or float8_e4m3fn with k_scale and v_scale fp32
-    [B, Hkv, Nk / BK].  blocks: int32 [B, H, ceil(Nq / C), kb] (a list ends at its first negative
-    entry), or None for every block.  kv_len: int32 [B], valid keys of each batch entry.  R: bf16
-    like Q, added to the result.  A row without a key gives R (0 without R) and lse = -inf."""
+def _plan_block_attn(Q, K, V, blocks, C, BK, R, kv_len, k_scale, v_scale, out, lse, scale):
     B, H, Nq, d = shape = _heads(Q, "Q")
     if not isinstance(K, torch.Tensor) or K.dtype not in (torch.bfloat16, E4M3):
         raise ValueError(f"K must be {torch.bfloat16} or {E4M3}")
@@ -566,37 +631,46 @@ def block_attn(Q, K, V, blocks, C: int, BK: int, R=None, kv_len=None, k_scale=No
     _length(kv_len, "kv_len", B)
     if R is not None:
         _spec(R, "R", torch.bfloat16, shape)
-    if out is None:
-        out = torch.empty_like(Q)
-    _spec(out, "out", torch.bfloat16, shape)
-    if want_lse and lse is None:
-        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=Q.device)
+    if out is not None:
+        _spec(out, "out", torch.bfloat16, shape)
     if lse is not None:
         _spec(lse, "lse", torch.float32, (B, H, Nq))
     _on_device(Q=Q, K=K, V=V, blocks=blocks, R=R, kv_len=kv_len, k_scale=k_scale, v_scale=v_scale, out=out, lse=lse)
-    _apart(dict(out=out, lse=lse), dict(Q=Q, K=K, V=V, R=R, blocks=blocks))
-    lib = _lib.load()
     s = _lib.BlockShape(B, H, Hkv, Nq, Nk, d, 0.0 if scale is None else float(scale))
-    if ws is None:
-        n = int(lib.mcs_block_attn_workspace_size(s, C, BK, kb))
-        if n == 0:
-            raise _lib.MCSError(2, "mcs_block_attn_workspace_size: invalid shape")
-        ws = torch.empty(n, dtype=torch.uint8, device=Q.device)
-    _spec(ws, "ws", torch.uint8)
-    _on_device(Q=Q, ws=ws)
-    check(lib.mcs_block_attn(s, ptr(Q), ptr(K), ptr(V), int(fp8), ptr(k_scale), ptr(v_scale), ptr(blocks), C, BK, kb,
-                             ptr(kv_len), ptr(R), ptr(out), ptr(lse), ptr(ws), ws.numel(), stream_ptr()),
+    n = int(_lib.load().mcs_block_attn_workspace_size(s, C, BK, kb))
+    if n == 0:
+        raise _lib.MCSError(2, "mcs_block_attn_workspace_size: invalid shape")
+    return s, kb, n, int(fp8)
+
+
+def block_attn(Q, K, V, blocks, C: int, BK: int, R=None, kv_len=None, k_scale=None, v_scale=None, out=None, lse=None,
+               want_lse: bool = False, ws=None, scale=None):
+    """Attention over the key blocks that each block of C query rows lists; returns (out, lse), lse
+    None unless wanted.
+
+    Q [B, H, Nq, d] bf16; K, V [B, Hkv, Nk, d] bf16, or float8_e4m3fn with k_scale and v_scale fp32
+    [B, Hkv, Nk / BK].  blocks: int32 [B, H, ceil(Nq / C), kb] (a list ends at its first negative
+    entry), or None for every block.  kv_len: int32 [B], valid keys of each batch entry.  R: bf16
+    like Q, added to the result.  A row without a key gives R (0 without R) and lse = -inf."""
+    key = _key("attn", (Q, K, V, blocks, R, kv_len, k_scale, v_scale, out, lse), C, BK, scale)
+    s, kb, n, fp8 = _plans.get(key) or _keep(key, _plan_block_attn(Q, K, V, blocks, C, BK, R, kv_len, k_scale, v_scale,
+                                                                   out, lse, scale))
+    dev = Q.device
+    _here(dev)
+    if out is not None or lse is not None:
+        _apart(dict(out=out, lse=lse), dict(Q=Q, K=K, V=V, R=R, blocks=blocks, kv_len=kv_len, k_scale=k_scale, v_scale=v_scale))
+    if out is None:
+        out = torch.empty_like(Q)
+    if want_lse and lse is None:
+        lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=dev)
+    ws = _workspace(ws, n, dev)
+    check(_lib.load().mcs_block_attn(s, _at(Q), _at(K), _at(V), fp8, _at(k_scale), _at(v_scale), _at(blocks), C, BK, kb,
+                                     _at(kv_len), _at(R), _at(out), _at(lse), _at(ws), ws.numel(), stream_ptr()),
           "mcs_block_attn")
     return out, lse
 
 
-def cache_write(K, V, K8, V8, k_scale, v_scale, BK: int, start: int = 0, means=None, lens=None):
-    """Write K and V (bf16 [B, H, n, d]) into rows [start, start + n) of an 8-bit store K8, V8
-    (float8_e4m3fn [B, H, capacity, d]) with one scale for each block of BK rows and head (fp32
-    [B, H, capacity / BK]), and each block's mean key into means (fp32 [B, H, capacity / BK, d]) if
-    given.  start and capacity are multiples of BK; a block's scale comes from this call's rows, so an
-    unfinished block is lengthened by writing its rows again.  lens: int32 [B], valid rows of this
-    call; rows behind them stay as they were."""
+def _plan_write(K, V, K8, V8, k_scale, v_scale, BK, start, means, lens):
     B, H, n, d = _heads(K, "K")
     _spec(V, "V", torch.bfloat16, (B, H, n, d))
     _block_sizes(BK=BK)
@@ -611,8 +685,21 @@ def cache_write(K, V, K8, V8, k_scale, v_scale, BK: int, start: int = 0, means=N
         _spec(means, "means", torch.float32, (B, H, cap // BK, d))
     _length(lens, "lens", B)
     _on_device(K=K, V=V, K8=K8, V8=V8, k_scale=k_scale, v_scale=v_scale, means=means, lens=lens)
-    check(_lib.load().mcs_cache_write(Shape(B, H, n, d, 0.0), ptr(K), ptr(V), BK, start, cap, ptr(lens), ptr(K8),
-                                      ptr(V8), ptr(k_scale), ptr(v_scale), ptr(means), stream_ptr()), "mcs_cache_write")
+    return Shape(B, H, n, d, 0.0), cap
+
+
+def cache_write(K, V, K8, V8, k_scale, v_scale, BK: int, start: int = 0, means=None, lens=None):
+    """Write K and V (bf16 [B, H, n, d]) into rows [start, start + n) of an 8-bit store K8, V8
+    (float8_e4m3fn [B, H, capacity, d]) with one scale for each block of BK rows and head (fp32
+    [B, H, capacity / BK]), and each block's mean key into means (fp32 [B, H, capacity / BK, d]) if
+    given.  start and capacity are multiples of BK; a block's scale comes from this call's rows, so an
+    unfinished block is lengthened by writing its rows again.  lens: int32 [B], valid rows of this
+    call; rows behind them stay as they were."""
+    key = _key("write", (K, V, K8, V8, k_scale, v_scale, means, lens), BK, start)
+    s, cap = _plans.get(key) or _keep(key, _plan_write(K, V, K8, V8, k_scale, v_scale, BK, start, means, lens))
+    _here(K.device)
+    check(_lib.load().mcs_cache_write(s, _at(K), _at(V), BK, start, cap, _at(lens), _at(K8), _at(V8), _at(k_scale),
+                                      _at(v_scale), _at(means), stream_ptr()), "mcs_cache_write")
 
 
 class KVCache:

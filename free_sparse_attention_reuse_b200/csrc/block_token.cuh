@@ -28,7 +28,7 @@ __device__ __forceinline__ void mma_16816(float& c0, float& c1, float& c2, float
 }
 // The same for at most 8 rows: the upper half of A is zero and that of the result is dropped.
 __device__ __forceinline__ void mma_8816(float& c0, float& c1, uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
-  float x, y;
+  [[maybe_unused]] float x, y;
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, {%0,%1,%9,%9};"
       : "+f"(c0), "+f"(c1), "=f"(x), "=f"(y)
       : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1), "f"(0.f));
