@@ -38,8 +38,7 @@ mcs_status block_device(DeviceInfo** out) {
   std::lock_guard<std::mutex> lock(g_mu);
   if (!(*out)->block_attrs_set) {
     const int topk = kTopkMaxBlocks * 8;
-    if (cudaFuncSetAttribute(block_topk_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, topk) != cudaSuccess ||
-        cudaFuncSetAttribute(block_topk_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, topk) != cudaSuccess ||
+    if (cudaFuncSetAttribute(block_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, topk) != cudaSuccess ||
         !block_attn_attrs<64, false, false>() || !block_attn_attrs<64, false, true>() ||
         !block_attn_attrs<64, true, false>() || !block_attn_attrs<64, true, true>() ||
         !block_attn_attrs<128, false, false>() || !block_attn_attrs<128, false, true>() ||
@@ -138,6 +137,60 @@ mcs_status run_block_attn(const BlockAttnParams& p, bool kv8, bool pair, cudaStr
   return pair ? run_block_attn<HD, false, true>(p, st, sms) : run_block_attn<HD, false, false>(p, st, sms);
 }
 
+void launch_means(int d, const __nv_bfloat16* X, const int32_t* len, float* means, int B, int H, int N, int BK,
+                  cudaStream_t st) {
+  MeansParams p{};
+  p.X = X;
+  p.len = len;
+  p.means = means;
+  p.H = H;
+  p.N = N;
+  p.BK = BK;
+  p.nb = (N + BK - 1) / BK;
+  p.blocks = static_cast<long long>(B) * H * p.nb;
+  const unsigned grid = static_cast<unsigned>((p.blocks + kMeansThreads / 32 - 1) / (kMeansThreads / 32));
+  if (d == 64) block_means_kernel<64><<<grid, kMeansThreads, 0, st>>>(p);
+  else block_means_kernel<128><<<grid, kMeansThreads, 0, st>>>(p);
+}
+
+// Workspace of mcs_block_topk: the score keys of as many rows as kTopkKeyBytes hold (all of them in most
+// calls; else the rows are worked off in parts, whole key heads or row ranges of one), then the mean
+// query rows.
+struct TopkPlan {
+  int M, kv_step, m_step;  // rows of a key head; key heads and rows of each in one part
+  size_t keys, total;
+};
+constexpr size_t kTopkKeyBytes = size_t{1} << 28;
+
+TopkPlan plan_topk(const mcs_block_shape& s, int C, int BK) {
+  TopkPlan q{};
+  const int GQ = (s.Nq + C - 1) / C, kvs = s.B * s.Hkv;
+  const size_t row = static_cast<size_t>((s.Nk + BK - 1) / BK) * 8;
+  q.M = s.H / s.Hkv * GQ;
+  const size_t fit = std::min<size_t>(std::max<size_t>(64, kTopkKeyBytes / row), size_t{1} << 21);  // rows (and grid)
+  q.kv_step = static_cast<int>(std::min<size_t>(kvs, std::max<size_t>(1, fit / q.M)));
+  q.m_step = static_cast<int>(std::min<size_t>(q.M, fit));
+  q.keys = round_up(row * q.kv_step * q.m_step, 256);
+  q.total = q.keys + (C > 1 ? round_up(static_cast<size_t>(s.B) * s.H * GQ * s.d * 4, 256) : 0);
+  return q;
+}
+
+template <int HD>
+void launch_topk(const TopkParams& p, int kvs, cudaStream_t st) {
+  const unsigned tiles = static_cast<unsigned>((p.nb + kScoreTile - 1) / kScoreTile);
+  // few rows: the tile form would spend its 64 rows on them (3 rows, 64 key heads: 30 us against 6)
+  if (p.mc <= kFewRows) block_score_few_kernel<HD><<<dim3(tiles, 1, kvs), 256, 0, st>>>(p);
+  else block_score_kernel<HD><<<dim3(tiles, (p.mc + kScoreTile - 1) / kScoreTile, kvs), 256, 0, st>>>(p);
+  const long long rows = static_cast<long long>(kvs) * p.mc;
+  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
+  if (p.nb <= 8 * 32) block_pick_warp_kernel<8><<<grid, 128, 0, st>>>(p, rows);
+  else if (p.nb <= 16 * 32) block_pick_warp_kernel<16><<<grid, 128, 0, st>>>(p, rows);
+  else if (p.nb <= 32 * 32) block_pick_warp_kernel<32><<<grid, 128, 0, st>>>(p, rows);
+  else
+    block_pick_kernel<<<static_cast<unsigned>(std::min<long long>(rows, 4096)), kTopkThreads,
+                        static_cast<size_t>(p.nb) * 8, st>>>(p, rows);
+}
+
 template <int HD, int NORM>
 void launch_rotary(const RotaryParams& p, bool halves, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(p.B) * static_cast<unsigned>(p.tiles);
@@ -234,26 +287,14 @@ mcs_status mcs_block_means(mcs_shape s, const void* X, int BK, const int32_t* le
   if (!aligned16(X) || !aligned16(means) || (reinterpret_cast<uintptr_t>(len) & 3u)) return MCS_ERR_DTYPE_ALIGN;
   DeviceInfo* di = nullptr;
   if ((e = block_device(&di)) != MCS_OK) return e;
-  MeansParams p{};
-  p.X = static_cast<const __nv_bfloat16*>(X);
-  p.len = len;
-  p.means = means;
-  p.H = s.H;
-  p.N = s.N;
-  p.BK = BK;
-  p.nb = (s.N + BK - 1) / BK;
-  p.blocks = static_cast<long long>(s.B) * s.H * p.nb;
-  const unsigned grid = static_cast<unsigned>((p.blocks + kMeansThreads / 32 - 1) / (kMeansThreads / 32));
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (s.d == 64) block_means_kernel<64><<<grid, kMeansThreads, 0, st>>>(p);
-  else block_means_kernel<128><<<grid, kMeansThreads, 0, st>>>(p);
+  launch_means(s.d, static_cast<const __nv_bfloat16*>(X), len, means, s.B, s.H, s.N, BK, static_cast<cudaStream_t>(stream));
   return launch_status();
 }
 
 size_t mcs_block_topk_workspace_size(mcs_block_shape s, int C, int BK) {
   if (check_block_shape(s) != MCS_OK || !query_rows_ok(C) || !block_rows_ok(BK) || (s.Nk + BK - 1) / BK > kTopkMaxBlocks)
     return 0;
-  return 256;
+  return plan_topk(s, C, BK).total;
 }
 
 mcs_status mcs_block_topk(mcs_block_shape s, const void* Q, const float* means, int C, int BK, int kb,
@@ -270,24 +311,35 @@ mcs_status mcs_block_topk(mcs_block_shape s, const void* Q, const float* means, 
   if (reinterpret_cast<uintptr_t>(ws) & 255u) return MCS_ERR_DTYPE_ALIGN;
   DeviceInfo* di = nullptr;
   if ((e = block_device(&di)) != MCS_OK) return e;
+  const TopkPlan plan = plan_topk(s, C, BK);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
   TopkParams p{};
   p.Q = static_cast<const __nv_bfloat16*>(Q);
   p.means = means;
   p.len = kv_len;
+  p.keys = static_cast<unsigned long long*>(ws);
   p.blocks = blocks;
-  p.H = s.H;
   p.Hkv = s.Hkv;
-  p.Nq = s.Nq;
   p.Nk = s.Nk;
-  p.GQ = (s.Nq + C - 1) / C;
-  p.C = C;
+  p.M = plan.M;
   p.BK = BK;
   p.nb = nb;
   p.kb = kb;
-  const dim3 grid(p.GQ, s.B * s.H);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (s.d == 64) block_topk_kernel<64><<<grid, kTopkThreads, static_cast<size_t>(nb) * 8, st>>>(p);
-  else block_topk_kernel<128><<<grid, kTopkThreads, static_cast<size_t>(nb) * 8, st>>>(p);
+  if (C > 1) {
+    float* qbar = reinterpret_cast<float*>(static_cast<char*>(ws) + plan.keys);
+    p.qbar = qbar;
+    launch_means(s.d, p.Q, nullptr, qbar, s.B, s.H, s.Nq, C, st);
+  }
+  const int kvs = s.B * s.Hkv;
+  for (int kv = 0; kv < kvs; kv += plan.kv_step)
+    for (int m = 0; m < plan.M; m += plan.m_step) {
+      p.kv0 = kv;
+      p.m0 = m;
+      p.mc = std::min(plan.m_step, plan.M - m);
+      const int kn = std::min(plan.kv_step, kvs - kv);
+      if (s.d == 64) launch_topk<64>(p, kn, st);
+      else launch_topk<128>(p, kn, st);
+    }
   return launch_status();
 }
 

@@ -69,104 +69,293 @@ __global__ void __launch_bounds__(kMeansThreads) block_means_kernel(const MeansP
 }
 
 // ---------------------------------------------------------------------------------- choice
-// Order of fp64 scores as unsigned integers; NaN below every number, both zeros alike.
+// score(g, j) = qbar_g . kbar_j of the fp32 means, in fp64 (their products are exact there), so that the
+// choice is the definition's and not a summation order's; then the kb largest of a row, ties to the lower
+// block.  Rows are query blocks; those of the H / Hkv heads that share a key head lie one behind the other
+// and make one matrix of M rows against its nb means.
+//
+// Order of scores as unsigned integers: 0 is no candidate, then NaN below every number, both zeros alike.
 __device__ __forceinline__ unsigned long long score_key(double s) {
-  if (s != s) return 0ull;
+  if (s != s) return 1ull;
   if (s == 0.0) s = 0.0;
   const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(s));
   return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
 
 struct TopkParams {
-  const __nv_bfloat16* Q;  // [B, H, Nq, d]
+  const __nv_bfloat16* Q;  // [B, H, Nq, d]: the rows themselves where C = 1
+  const float* qbar;       // [B, H, GQ, d]: their means else
   const float* means;      // [B, Hkv, nb, d]
   const int32_t* len;      // [B], nullable
-  int32_t* blocks;         // [B, H, GQ, kb]
-  int H, Hkv, Nq, Nk, GQ, C, BK, nb, kb;
+  unsigned long long* keys;  // [rows of this launch, nb]
+  int32_t* blocks;           // [B, H, GQ, kb]
+  int Hkv, Nk, M, BK, nb, kb;
+  int kv0, m0, mc;  // rows of this launch: key heads from kv0 on (the grid's), rows [m0, m0 + mc) of each
 };
+
+__device__ __forceinline__ int candidate_blocks(const TopkParams& p, int kv) {
+  return (valid_rows(p.len, kv / p.Hkv, p.Nk) + p.BK - 1) / p.BK;
+}
+
+// 64 rows by 64 blocks a CTA, 4 x 4 a thread, 32 columns of d at a time from shared memory.  Bound: the
+// fp64 pipe (195 M multiply-adds for 24 heads of 252 x 252 blocks of 128: 11 us at its full rate).
+constexpr int kScoreTile = 64, kScoreDepth = 32;
+
+template <int HD>
+__global__ void __launch_bounds__(256) block_score_kernel(const TopkParams p) {
+  constexpr int LD = kScoreTile + 2;
+  __shared__ __align__(16) double as[kScoreDepth][LD], bs[kScoreDepth][LD];
+  const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
+  const int kv = p.kv0 + blockIdx.z, m0 = blockIdx.y * kScoreTile, j0 = blockIdx.x * kScoreTile;
+  const int nv = candidate_blocks(p, kv);
+  if (j0 >= nv) return;
+  const size_t row0 = static_cast<size_t>(kv) * p.M + p.m0 + m0;
+  const int rows = p.mc - m0;
+  double acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.0;
+  for (int k0 = 0; k0 < HD; k0 += kScoreDepth) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = (t >> 3) + 32 * i, k = (t & 7) * 4;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+      if (r < rows) {
+        const size_t at = (row0 + r) * HD + k0 + k;
+        if (p.qbar != nullptr) {
+          a = *reinterpret_cast<const float4*>(p.qbar + at);
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(p.Q + at);
+          const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+          const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+          a = make_float4(x.x, x.y, y.x, y.y);
+        }
+      }
+      if (j0 + r < nv) b = *reinterpret_cast<const float4*>(p.means + (static_cast<size_t>(kv) * p.nb + j0 + r) * HD + k0 + k);
+      as[k][r] = a.x, as[k + 1][r] = a.y, as[k + 2][r] = a.z, as[k + 3][r] = a.w;
+      bs[k][r] = b.x, bs[k + 1][r] = b.y, bs[k + 2][r] = b.z, bs[k + 3][r] = b.w;
+    }
+    __syncthreads();
+#pragma unroll 8
+    for (int k = 0; k < kScoreDepth; ++k) {
+      double x[4], y[4];
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        const double2 u = *reinterpret_cast<const double2*>(&as[k][ty * 4 + i]);
+        const double2 v = *reinterpret_cast<const double2*>(&bs[k][tx * 4 + i]);
+        x[i] = u.x, x[i + 1] = u.y, y[i] = v.x, y[i + 1] = v.y;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fma(x[i], y[j], acc[i][j]);
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty * 4 + i;
+    if (r >= rows) continue;
+    unsigned long long* out = p.keys + (static_cast<size_t>(blockIdx.z) * p.mc + m0 + r) * p.nb;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = j0 + tx * 4 + j;
+      if (c < nv) out[c] = score_key(acc[i][j]);
+    }
+  }
+}
+
+// At most kFewRows rows (one token): every mean is read once, HD / 4 lanes to a block, the rows in
+// registers.  Bound: reading the means (33.5 MB for 64 key heads of 1024 blocks of 128: 5 us).
+constexpr int kFewRows = 4;
+
+template <int HD>
+__global__ void __launch_bounds__(256) block_score_few_kernel(const TopkParams p) {
+  constexpr int LPR = HD / 4, RPW = 32 / LPR;  // lanes to a block, blocks of a warp's load
+  const int lane = lane_id(), c = lane % LPR, sub = lane / LPR;
+  const int kv = p.kv0 + blockIdx.z;
+  const int nv = candidate_blocks(p, kv);
+  const int j0 = blockIdx.x * 64 + warp_id() * 8;
+  if (j0 >= nv) return;
+  double q[kFewRows][4];
+#pragma unroll
+  for (int r = 0; r < kFewRows; ++r) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q[r][e] = 0.0;
+    if (r >= p.mc) continue;
+    const size_t at = (static_cast<size_t>(kv) * p.M + p.m0 + r) * HD + c * 4;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      q[r][e] = p.qbar != nullptr ? static_cast<double>(p.qbar[at + e]) : static_cast<double>(__bfloat162float(p.Q[at + e]));
+  }
+  constexpr int IT = 8 / RPW;
+  float4 v[IT];
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int j = j0 + i * RPW + sub;
+    v[i] = j < nv ? *reinterpret_cast<const float4*>(p.means + (static_cast<size_t>(kv) * p.nb + j) * HD + c * 4)
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int j = j0 + i * RPW + sub;
+#pragma unroll
+    for (int r = 0; r < kFewRows; ++r) {
+      if (r >= p.mc) break;
+      double s = q[r][0] * static_cast<double>(v[i].x);
+      s = fma(q[r][1], static_cast<double>(v[i].y), s);
+      s = fma(q[r][2], static_cast<double>(v[i].z), s);
+      s = fma(q[r][3], static_cast<double>(v[i].w), s);
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (c == 0 && j < nv) p.keys[(static_cast<size_t>(blockIdx.z) * p.mc + r) * p.nb + j] = score_key(s);
+    }
+  }
+}
+
+// The kb largest keys of a row, one warp a row with its keys in registers (nb <= 32 KPL): the kk-th
+// largest high word bit by bit, by counting; the low words only where the cut falls among equal high words.
+template <int KPL>
+__global__ void __launch_bounds__(128) block_pick_warp_kernel(const TopkParams p, long long rows) {
+  const long long r = static_cast<long long>(blockIdx.x) * 4 + warp_id();
+  if (r >= rows) return;
+  const int lane = lane_id();
+  const int kv = p.kv0 + static_cast<int>(r / p.mc);
+  const int nv = candidate_blocks(p, kv), kk = min(p.kb, nv);
+  const unsigned long long* keys = p.keys + static_cast<size_t>(r) * p.nb;
+  int32_t* out = p.blocks + (static_cast<size_t>(kv) * p.M + p.m0 + static_cast<int>(r % p.mc)) * p.kb;
+  uint32_t w[KPL];  // high words, then the low words of the keys at the cut
+#pragma unroll
+  for (int i = 0; i < KPL; ++i) {
+    const int j = i * 32 + lane;
+    w[i] = j < nv ? static_cast<uint32_t>(keys[j] >> 32) : 0u;
+  }
+  auto count = [&](uint32_t cand) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) n += w[i] >= cand ? 1 : 0;
+    return __reduce_add_sync(0xffffffffu, n);
+  };
+  // the largest cut that at least `want` words reach; `reach` = how many do (all for cut 0)
+  auto search = [&](int want, int all, int& reach) {
+    uint32_t cut = 0;
+    reach = all;
+    for (int bit = 31; bit >= 0 && reach != want; --bit) {
+      const uint32_t cand = cut | (1u << bit);
+      const int n = count(cand);
+      if (n >= want) cut = cand, reach = n;
+    }
+    return cut;
+  };
+  uint32_t chosen = 0, at_cut = 0;  // bit i: key 32 i + lane
+  int reach;
+  uint32_t cut = search(kk, nv, reach);
+  int ties = 0;  // keys to take of those at the cut
+#pragma unroll
+  for (int i = 0; i < KPL; ++i) {
+    const bool in = i * 32 + lane < nv;
+    if (in && (w[i] > cut || (reach == kk && w[i] == cut))) chosen |= 1u << i;
+    if (in && reach != kk && w[i] == cut) at_cut |= 1u << i;
+  }
+  if (reach != kk) {
+    const int eq = __reduce_add_sync(0xffffffffu, __popc(at_cut));
+    ties = kk - (reach - eq);
+    // low words + 1 would overflow: a key at the cut whose low word is 0 counts for cut 0 alone
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) w[i] = at_cut >> i & 1u ? static_cast<uint32_t>(keys[i * 32 + lane]) : 0u;
+    cut = search(ties, eq, reach);
+    uint32_t rest = 0;
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) {
+      if (!(at_cut >> i & 1u)) continue;
+      if (w[i] > cut || (reach == ties && w[i] == cut)) chosen |= 1u << i;
+      else if (w[i] == cut) rest |= 1u << i;
+    }
+    ties = reach == ties ? 0 : ties - (reach - __reduce_add_sync(0xffffffffu, __popc(rest)));
+    at_cut = rest;
+  }
+  int base = 0, tied = 0;
+  const uint32_t lt = (1u << lane) - 1u;
+#pragma unroll
+  for (int i = 0; i < KPL; ++i) {
+    bool take = chosen >> i & 1u;
+    if (ties > 0) {
+      const uint32_t eq = __ballot_sync(0xffffffffu, at_cut >> i & 1u);
+      take |= (at_cut >> i & 1u) && tied + __popc(eq & lt) < ties;
+      tied += __popc(eq);
+    }
+    const uint32_t got = __ballot_sync(0xffffffffu, take);
+    if (take) out[base + __popc(got & lt)] = i * 32 + lane;
+    base += __popc(got);
+  }
+  for (int i = kk + lane; i < p.kb; i += 32) out[i] = -1;
+}
 
 constexpr int kTopkThreads = 256;
 constexpr int kTopkMaxBlocks = 24576;  // keys of a row in shared memory: 8 bytes each
 
-// One query block: qbar (mean of its rows), s_j = qbar . kbar_j, the kb largest, ties to the lower j.
-// Scores are fp64 (the fp32 means' products are exact there), so that the choice is the definition's
-// and not the summation order's.
-template <int HD>
-__global__ void __launch_bounds__(kTopkThreads) block_topk_kernel(const TopkParams p) {
+// The same for longer rows, a CTA a row with its keys in shared memory.
+__global__ void __launch_bounds__(kTopkThreads) block_pick_kernel(const TopkParams p, long long rows) {
   extern __shared__ __align__(16) unsigned long long tkeys[];  // nb
-  __shared__ double qbar[HD];
   __shared__ int red[kTopkThreads / 32];
   const int t = threadIdx.x, lane = lane_id(), warp = warp_id();
-  const int g = blockIdx.x, bh = blockIdx.y;
-  const int b = bh / p.H, h = bh - b * p.H;
-  const int nq = min(p.C, p.Nq - g * p.C);
-  if (t < HD) {
-    const __nv_bfloat16* q = p.Q + (static_cast<size_t>(bh) * p.Nq + static_cast<size_t>(g) * p.C) * HD + t;
-    double acc = 0.0;
-    for (int r = 0; r < nq; ++r) acc += static_cast<double>(__bfloat162float(q[static_cast<size_t>(r) * HD]));
-    qbar[t] = static_cast<double>(static_cast<float>(acc / static_cast<double>(nq)));
-  }
-  __syncthreads();
-  const int nv = (valid_rows(p.len, b, p.Nk) + p.BK - 1) / p.BK;  // blocks with a valid key
-  const int kk = min(p.kb, nv);
-  const float* mk = p.means + (static_cast<size_t>(b) * p.Hkv + h / (p.H / p.Hkv)) * p.nb * HD;
-  for (int j = t; j < nv; j += kTopkThreads) {
-    double acc = 0.0;
-    for (int c = 0; c < HD; ++c) acc = fma(qbar[c], static_cast<double>(mk[static_cast<size_t>(j) * HD + c]), acc);
-    tkeys[j] = score_key(acc);
-  }
-  __syncthreads();
-  auto count = [&](unsigned long long cand) {  // keys >= cand
-    int n = 0;
-    for (int j = t; j < nv; j += kTopkThreads) n += tkeys[j] >= cand ? 1 : 0;
-    n = __reduce_add_sync(0xffffffffu, n);
+  for (long long r = blockIdx.x; r < rows; r += gridDim.x) {
+    const int kv = p.kv0 + static_cast<int>(r / p.mc);
+    const int nv = candidate_blocks(p, kv), kk = min(p.kb, nv);
+    const unsigned long long* keys = p.keys + static_cast<size_t>(r) * p.nb;
+    int32_t* out = p.blocks + (static_cast<size_t>(kv) * p.M + p.m0 + static_cast<int>(r % p.mc)) * p.kb;
+    __syncthreads();  // the row before this one is done with the keys
+    for (int j = t; j < nv; j += kTopkThreads) tkeys[j] = keys[j];
     __syncthreads();
-    if (lane == 0) red[warp] = n;
-    __syncthreads();
-    n = 0;
-    for (int i = 0; i < kTopkThreads / 32; ++i) n += red[i];
-    return n;
-  };
-  // the kk-th largest key, bit by bit; `above` = keys larger than it once every bit is fixed
-  unsigned long long cut = 0;
-  int at_cut = nv;  // keys >= cut
-  for (int bit = 63; bit >= 0 && at_cut != kk; --bit) {
-    const unsigned long long cand = cut | (1ull << bit);
-    const int n = count(cand);
-    if (n >= kk) {
-      cut = cand;
-      at_cut = n;
+    auto count = [&](unsigned long long cand) {  // keys >= cand
+      int n = 0;
+      for (int j = t; j < nv; j += kTopkThreads) n += tkeys[j] >= cand ? 1 : 0;
+      n = __reduce_add_sync(0xffffffffu, n);
+      __syncthreads();
+      if (lane == 0) red[warp] = n;
+      __syncthreads();
+      n = 0;
+      for (int i = 0; i < kTopkThreads / 32; ++i) n += red[i];
+      return n;
+    };
+    // the kk-th largest key, bit by bit; at_cut = keys that reach it
+    unsigned long long cut = 0;
+    int at_cut = nv;
+    for (int bit = 63; bit >= 0 && at_cut != kk; --bit) {
+      const unsigned long long cand = cut | (1ull << bit);
+      const int n = count(cand);
+      if (n >= kk) cut = cand, at_cut = n;
     }
-  }
-  // keys above the cut, and of those equal to it the first `ties`
-  int ties = kk;
-  if (at_cut != kk) ties = kk - (cut == ~0ull ? 0 : count(cut + 1));
-  int32_t* out = p.blocks + (static_cast<size_t>(bh) * p.GQ + g) * p.kb;
-  int base = 0, eq_base = 0;
-  for (int j0 = 0; j0 < nv; j0 += kTopkThreads) {
-    const int j = j0 + t;
-    const unsigned long long k = j < nv ? tkeys[j] : 0ull;
-    const bool eq = j < nv && at_cut != kk && k == cut;
-    const bool gt = j < nv && (at_cut != kk ? k > cut : k >= cut);
-    // counts of both kinds in the warps before this one, packed in one word
-    const unsigned beq = __ballot_sync(0xffffffffu, eq), bgt = __ballot_sync(0xffffffffu, gt);
-    __syncthreads();
-    if (lane == 0) red[warp] = __popc(bgt) | (__popc(beq) << 16);
-    __syncthreads();
-    int gt_before = 0, eq_before = 0, gt_all = 0, eq_all = 0;
-    for (int i = 0; i < kTopkThreads / 32; ++i) {
-      const int v = red[i];
-      if (i < warp) gt_before += v & 0xffff, eq_before += v >> 16;
-      gt_all += v & 0xffff, eq_all += v >> 16;
+    // keys above the cut, and of those equal to it the first `ties`
+    int ties = kk;
+    if (at_cut != kk) ties = kk - (cut == ~0ull ? 0 : count(cut + 1));
+    int base = 0, eq_base = 0;
+    for (int j0 = 0; j0 < nv; j0 += kTopkThreads) {
+      const int j = j0 + t;
+      const unsigned long long k = j < nv ? tkeys[j] : 0ull;
+      const bool eq = j < nv && at_cut != kk && k == cut;
+      const bool gt = j < nv && (at_cut != kk ? k > cut : k >= cut);
+      // counts of both kinds in the warps before this one, packed in one word
+      const unsigned beq = __ballot_sync(0xffffffffu, eq), bgt = __ballot_sync(0xffffffffu, gt);
+      __syncthreads();
+      if (lane == 0) red[warp] = __popc(bgt) | (__popc(beq) << 16);
+      __syncthreads();
+      int gt_before = 0, eq_before = 0, gt_all = 0, eq_all = 0;
+      for (int i = 0; i < kTopkThreads / 32; ++i) {
+        const int v = red[i];
+        if (i < warp) gt_before += v & 0xffff, eq_before += v >> 16;
+        gt_all += v & 0xffff, eq_all += v >> 16;
+      }
+      const unsigned lt = (1u << lane) - 1u;
+      const int eq_rank = eq_base + eq_before + __popc(beq & lt);  // this key's place among the equal ones
+      const int gt_rank = base + gt_before + __popc(bgt & lt);     // chosen keys above the cut before it
+      if (gt || (eq && eq_rank < ties)) out[gt_rank + min(eq_rank, ties)] = j;
+      base += gt_all;
+      eq_base += eq_all;
     }
-    const unsigned lt = (1u << lane) - 1u;
-    const int eq_rank = eq_base + eq_before + __popc(beq & lt);     // this key's place among the equal ones
-    const int gt_rank = base + gt_before + __popc(bgt & lt);        // chosen keys above the cut before it
-    if (gt || (eq && eq_rank < ties)) out[gt_rank + min(eq_rank, ties)] = j;
-    base += gt_all;
-    eq_base += eq_all;
+    for (int i = kk + t; i < p.kb; i += kTopkThreads) out[i] = -1;
   }
-  for (int i = kk + t; i < p.kb; i += kTopkThreads) out[i] = -1;
 }
 
 // ---------------------------------------------------------------------------------- 8-bit store

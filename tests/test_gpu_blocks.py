@@ -133,6 +133,9 @@ def _check_topk(got, want, scores, kb):
     (2, 3, 3, 7, 129, 64, 1, 128, 1, [1, 129]),
     (1, 2, 1, 1000, 20000, 64, 16, 32, 300, None),
     (1, 1, 1, 3, 70000, 128, 1, 32, 2000, None),
+    (1, 2, 2, 300, 14000, 64, 64, 32, 60, [13000]),
+    (2, 3, 1, 1, 40000, 64, 1, 64, 100, [40000, 12345]),
+    (1, 6, 1, 200, 300, 64, 64, 128, 2, None),
 ])
 def test_block_topk(B, H, Hkv, Nq, Nk, d, C, BK, kb, lens):
     q, k = rnd(8, B, H, Nq, d), rnd(9, B, Hkv, Nk, d)
