@@ -161,6 +161,7 @@ struct TopkPlan {
   size_t keys, total;
 };
 constexpr size_t kTopkKeyBytes = size_t{1} << 28;
+constexpr long long kPickWarpRows = 2048;
 
 TopkPlan plan_topk(const mcs_block_shape& s, int C, int BK) {
   TopkPlan q{};
@@ -178,14 +179,16 @@ TopkPlan plan_topk(const mcs_block_shape& s, int C, int BK) {
 template <int HD>
 void launch_topk(const TopkParams& p, int kvs, cudaStream_t st) {
   const unsigned tiles = static_cast<unsigned>((p.nb + kScoreTile - 1) / kScoreTile);
+  static_assert(kScoreTile == kFewBlocks, "one grid for both forms");
   // few rows: the tile form would spend its 64 rows on them (3 rows, 64 key heads: 30 us against 6)
-  if (p.mc <= kFewRows) block_score_few_kernel<HD><<<dim3(tiles, 1, kvs), 256, 0, st>>>(p);
-  else block_score_kernel<HD><<<dim3(tiles, (p.mc + kScoreTile - 1) / kScoreTile, kvs), 256, 0, st>>>(p);
+  if (p.mc <= kFewRows) block_score_few_kernel<HD><<<dim3(tiles, 1, kvs), 128, 0, st>>>(p);
+  else block_score_kernel<HD><<<dim3(tiles, (p.mc + kScoreTile - 1) / kScoreTile, kvs), kScoreThreads, 0, st>>>(p);
   const long long rows = static_cast<long long>(kvs) * p.mc;
   const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-  if (p.nb <= 8 * 32) block_pick_warp_kernel<8><<<grid, 128, 0, st>>>(p, rows);
-  else if (p.nb <= 16 * 32) block_pick_warp_kernel<16><<<grid, 128, 0, st>>>(p, rows);
-  else if (p.nb <= 32 * 32) block_pick_warp_kernel<32><<<grid, 128, 0, st>>>(p, rows);
+  const bool warps = rows >= kPickWarpRows;  // enough of them to fill the GPU with a warp each
+  if (warps && p.nb <= 8 * 32) block_pick_warp_kernel<8><<<grid, 128, 0, st>>>(p, rows);
+  else if (warps && p.nb <= 16 * 32) block_pick_warp_kernel<16><<<grid, 128, 0, st>>>(p, rows);
+  else if (warps && p.nb <= 32 * 32) block_pick_warp_kernel<32><<<grid, 128, 0, st>>>(p, rows);
   else
     block_pick_kernel<<<static_cast<unsigned>(std::min<long long>(rows, 4096)), kTopkThreads,
                         static_cast<size_t>(p.nb) * 8, st>>>(p, rows);
@@ -269,8 +272,9 @@ mcs_status mcs_rotary(const mcs_rotary_args* a, const void* q, const void* k, co
   p.pos_batch = a->pos_per_batch != 0;
   p.w_bf16 = a->weight_is_bf16 != 0;
   p.eps = a->eps;
-  // 16 tokens a CTA (4 KB of consecutive output per head at d = 128) unless that leaves SMs idle
-  p.T = kRotMaxTokens;
+  // a token for every group of lanes of a CTA, fewer tokens (a token's heads shared among groups) where
+  // that leaves SMs idle
+  p.T = kRotThreads / (a->d / 8);
   while (p.T > 1 && static_cast<long long>(a->B) * ((a->N + p.T - 1) / p.T) < 2ll * di->sms) p.T /= 2;
   p.tiles = (a->N + p.T - 1) / p.T;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -3,6 +3,8 @@
 
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "rotary.cuh"
 
 namespace mcs {
@@ -32,7 +34,7 @@ struct MeansParams {
   long long blocks;        // B * H * nb
 };
 
-constexpr int kMeansThreads = 256;
+constexpr int kMeansThreads = 128;
 
 template <int HD>
 __global__ void __launch_bounds__(kMeansThreads) block_means_kernel(const MeansParams p) {
@@ -47,13 +49,21 @@ __global__ void __launch_bounds__(kMeansThreads) block_means_kernel(const MeansP
   double acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.0;
-#pragma unroll 4
-  for (int r = sub; r < n; r += RPW) {
+  auto add = [&](const uint4& u) {
     float f[8];
-    unpack8(*reinterpret_cast<const uint4*>(row + static_cast<size_t>(r) * HD), f);
+    unpack8(u, f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] += static_cast<double>(f[i]);
+  };
+  int r = sub;
+  for (; r + 7 * RPW < n; r += 8 * RPW) {  // eight rows in flight
+    uint4 u[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) u[k] = load16(row + static_cast<size_t>(r + k * RPW) * HD);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) add(u[k]);
   }
+  for (; r < n; r += RPW) add(load16(row + static_cast<size_t>(r) * HD));
 #pragma unroll
   for (int o = LPR; o < 32; o <<= 1)
 #pragma unroll
@@ -97,65 +107,81 @@ __device__ __forceinline__ int candidate_blocks(const TopkParams& p, int kv) {
   return (valid_rows(p.len, kv / p.Hkv, p.Nk) + p.BK - 1) / p.BK;
 }
 
-// 64 rows by 64 blocks a CTA, 4 x 4 a thread, 32 columns of d at a time from shared memory.  Bound: the
-// fp64 pipe (195 M multiply-adds for 24 heads of 252 x 252 blocks of 128: 11 us at its full rate).
-constexpr int kScoreTile = 64, kScoreDepth = 32;
+// 64 rows by 64 blocks a CTA, 8 x 4 a thread, 32 columns of d at a time from shared memory (columns in
+// groups of four, the group's place XORed with its row's so that the transposing stores spread over the
+// banks).  Bound: the fp64 pipe (195 M multiply-adds for 24 heads of 252 x 252 blocks of 128: 11 us at its
+// full rate); 4 x 4 a thread was bound by the reads of shared memory (48 us).
+constexpr int kScoreTile = 64, kScoreDepth = 32, kScoreThreads = 128;
 
 template <int HD>
-__global__ void __launch_bounds__(256) block_score_kernel(const TopkParams p) {
-  constexpr int LD = kScoreTile + 2;
-  __shared__ __align__(16) double as[kScoreDepth][LD], bs[kScoreDepth][LD];
+__global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const TopkParams p) {
+  __shared__ __align__(16) double as[kScoreDepth][kScoreTile], bs[kScoreDepth][kScoreTile];
   const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
   const int kv = p.kv0 + blockIdx.z, m0 = blockIdx.y * kScoreTile, j0 = blockIdx.x * kScoreTile;
   const int nv = candidate_blocks(p, kv);
   if (j0 >= nv) return;
   const size_t row0 = static_cast<size_t>(kv) * p.M + p.m0 + m0;
   const int rows = p.mc - m0;
-  double acc[4][4];
+  double acc[8][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.0;
-  for (int k0 = 0; k0 < HD; k0 += kScoreDepth) {
+  float4 a[4], b[4];
+  auto load = [&](int k0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = (t >> 3) + 32 * i, k = (t & 7) * 4;
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    for (int i = 0; i < 4; ++i) {
+      const int r = (t >> 3) + 16 * i, k = (t & 7) * 4;
+      a[i] = b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows) {
         const size_t at = (row0 + r) * HD + k0 + k;
         if (p.qbar != nullptr) {
-          a = *reinterpret_cast<const float4*>(p.qbar + at);
+          a[i] = *reinterpret_cast<const float4*>(p.qbar + at);
         } else {
           const uint2 u = *reinterpret_cast<const uint2*>(p.Q + at);
           const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
           const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-          a = make_float4(x.x, x.y, y.x, y.y);
+          a[i] = make_float4(x.x, x.y, y.x, y.y);
         }
       }
-      if (j0 + r < nv) b = *reinterpret_cast<const float4*>(p.means + (static_cast<size_t>(kv) * p.nb + j0 + r) * HD + k0 + k);
-      as[k][r] = a.x, as[k + 1][r] = a.y, as[k + 2][r] = a.z, as[k + 3][r] = a.w;
-      bs[k][r] = b.x, bs[k + 1][r] = b.y, bs[k + 2][r] = b.z, bs[k + 3][r] = b.w;
+      if (j0 + r < nv) b[i] = *reinterpret_cast<const float4*>(p.means + (static_cast<size_t>(kv) * p.nb + j0 + r) * HD + k0 + k);
+    }
+  };
+  load(0);
+  for (int k0 = 0; k0 < HD; k0 += kScoreDepth) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = (t >> 3) + 16 * i, k = (t & 7) * 4;
+      const int at = (((r >> 2) ^ (t & 7)) << 2) | (r & 3);
+      as[k][at] = a[i].x, as[k + 1][at] = a[i].y, as[k + 2][at] = a[i].z, as[k + 3][at] = a[i].w;
+      bs[k][at] = b[i].x, bs[k + 1][at] = b[i].y, bs[k + 2][at] = b[i].z, bs[k + 3][at] = b[i].w;
     }
     __syncthreads();
-#pragma unroll 8
+    if (k0 + kScoreDepth < HD) load(k0 + kScoreDepth);
+#pragma unroll 4
     for (int k = 0; k < kScoreDepth; ++k) {
-      double x[4], y[4];
+      double x[8], y[4];
+      const int sw = k >> 2;
 #pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        const double2 u = *reinterpret_cast<const double2*>(&as[k][ty * 4 + i]);
-        const double2 v = *reinterpret_cast<const double2*>(&bs[k][tx * 4 + i]);
-        x[i] = u.x, x[i + 1] = u.y, y[i] = v.x, y[i + 1] = v.y;
+      for (int i = 0; i < 8; i += 2) {
+        const double2 u = *reinterpret_cast<const double2*>(&as[k][(((ty * 2 + (i >> 2)) ^ sw) << 2) + (i & 3)]);
+        x[i] = u.x, x[i + 1] = u.y;
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; i += 2) {
+        const double2 v = *reinterpret_cast<const double2*>(&bs[k][((tx ^ sw) << 2) + i]);
+        y[i] = v.x, y[i + 1] = v.y;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = fma(x[i], y[j], acc[i][j]);
     }
-    __syncthreads();
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = ty * 4 + i;
+  for (int i = 0; i < 8; ++i) {
+    const int r = ty * 8 + i;
     if (r >= rows) continue;
     unsigned long long* out = p.keys + (static_cast<size_t>(blockIdx.z) * p.mc + m0 + r) * p.nb;
 #pragma unroll
@@ -166,49 +192,53 @@ __global__ void __launch_bounds__(256) block_score_kernel(const TopkParams p) {
   }
 }
 
-// At most kFewRows rows (one token): every mean is read once, HD / 4 lanes to a block, the rows in
-// registers.  Bound: reading the means (33.5 MB for 64 key heads of 1024 blocks of 128: 5 us).
-constexpr int kFewRows = 4;
+// At most kFewRows rows (one token): every mean is read once, eight lanes to a block, the rows in shared
+// memory.  Bound: reading the means (33.5 MB for 64 key heads of 1024 blocks of 128: 5 us).
+constexpr int kFewRows = 4, kFewBlocks = 64;  // rows; blocks a CTA of four warps takes
 
 template <int HD>
-__global__ void __launch_bounds__(256) block_score_few_kernel(const TopkParams p) {
-  constexpr int LPR = HD / 4, RPW = 32 / LPR;  // lanes to a block, blocks of a warp's load
-  const int lane = lane_id(), c = lane % LPR, sub = lane / LPR;
+__global__ void __launch_bounds__(128) block_score_few_kernel(const TopkParams p) {
+  constexpr int CH = HD / 32;  // 4-column pieces of a lane
+  __shared__ __align__(16) double q[kFewRows][HD];
+  const int lane = lane_id(), c = lane & 7, sub = lane >> 3;
   const int kv = p.kv0 + blockIdx.z;
   const int nv = candidate_blocks(p, kv);
-  const int j0 = blockIdx.x * 64 + warp_id() * 8;
-  if (j0 >= nv) return;
-  double q[kFewRows][4];
-#pragma unroll
-  for (int r = 0; r < kFewRows; ++r) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) q[r][e] = 0.0;
-    if (r >= p.mc) continue;
-    const size_t at = (static_cast<size_t>(kv) * p.M + p.m0 + r) * HD + c * 4;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      q[r][e] = p.qbar != nullptr ? static_cast<double>(p.qbar[at + e]) : static_cast<double>(__bfloat162float(p.Q[at + e]));
-  }
-  constexpr int IT = 8 / RPW;
-  float4 v[IT];
+  const int j0 = blockIdx.x * kFewBlocks + warp_id() * (kFewBlocks / 4);
+  constexpr int IT = kFewBlocks / 16;
+  float4 v[IT][CH];
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
-    const int j = j0 + i * RPW + sub;
-    v[i] = j < nv ? *reinterpret_cast<const float4*>(p.means + (static_cast<size_t>(kv) * p.nb + j) * HD + c * 4)
-                  : make_float4(0.f, 0.f, 0.f, 0.f);
+    const int j = j0 + i * 4 + sub;
+#pragma unroll
+    for (int h = 0; h < CH; ++h)
+      v[i][h] = j < nv ? *reinterpret_cast<const float4*>(p.means + (static_cast<size_t>(kv) * p.nb + j) * HD + h * 32 + c * 4)
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  for (int i = threadIdx.x; i < p.mc * HD; i += 128) {
+    const int r = i / HD, e = i - r * HD;
+    const size_t at = (static_cast<size_t>(kv) * p.M + p.m0 + r) * HD + e;
+    q[r][e] = p.qbar != nullptr ? static_cast<double>(p.qbar[at]) : static_cast<double>(__bfloat162float(p.Q[at]));
+  }
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
-    const int j = j0 + i * RPW + sub;
+    const int j = j0 + i * 4 + sub;
+    double x[CH * 4];
 #pragma unroll
-    for (int r = 0; r < kFewRows; ++r) {
-      if (r >= p.mc) break;
-      double s = q[r][0] * static_cast<double>(v[i].x);
-      s = fma(q[r][1], static_cast<double>(v[i].y), s);
-      s = fma(q[r][2], static_cast<double>(v[i].z), s);
-      s = fma(q[r][3], static_cast<double>(v[i].w), s);
+    for (int h = 0; h < CH; ++h) x[4 * h] = v[i][h].x, x[4 * h + 1] = v[i][h].y, x[4 * h + 2] = v[i][h].z, x[4 * h + 3] = v[i][h].w;
+    for (int r = 0; r < p.mc; ++r) {
+      double s = 0.0;
 #pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      for (int h = 0; h < CH; ++h) {
+        const double2 y = *reinterpret_cast<const double2*>(&q[r][h * 32 + c * 4]);
+        const double2 z = *reinterpret_cast<const double2*>(&q[r][h * 32 + c * 4 + 2]);
+        s = fma(x[4 * h], y.x, s);
+        s = fma(x[4 * h + 1], y.y, s);
+        s = fma(x[4 * h + 2], z.x, s);
+        s = fma(x[4 * h + 3], z.y, s);
+      }
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       if (c == 0 && j < nv) p.keys[(static_cast<size_t>(blockIdx.z) * p.mc + r) * p.nb + j] = score_key(s);
     }
   }
@@ -295,10 +325,12 @@ __global__ void __launch_bounds__(128) block_pick_warp_kernel(const TopkParams p
 constexpr int kTopkThreads = 256;
 constexpr int kTopkMaxBlocks = 24576;  // keys of a row in shared memory: 8 bytes each
 
-// The same for longer rows, a CTA a row with its keys in shared memory.
+// The same, a CTA a row with its keys in shared memory: longer rows, and few rows (192 rows of 1024: 11.5 us
+// with a warp each).  Two bits a step: the counts of three candidates in one 64-bit sum.
 __global__ void __launch_bounds__(kTopkThreads) block_pick_kernel(const TopkParams p, long long rows) {
   extern __shared__ __align__(16) unsigned long long tkeys[];  // nb
-  __shared__ int red[kTopkThreads / 32];
+  constexpr int WARPS = kTopkThreads / 32;
+  __shared__ unsigned long long red[2][WARPS];
   const int t = threadIdx.x, lane = lane_id(), warp = warp_id();
   for (long long r = blockIdx.x; r < rows; r += gridDim.x) {
     const int kv = p.kv0 + static_cast<int>(r / p.mc);
@@ -308,28 +340,39 @@ __global__ void __launch_bounds__(kTopkThreads) block_pick_kernel(const TopkPara
     __syncthreads();  // the row before this one is done with the keys
     for (int j = t; j < nv; j += kTopkThreads) tkeys[j] = keys[j];
     __syncthreads();
-    auto count = [&](unsigned long long cand) {  // keys >= cand
-      int n = 0;
-      for (int j = t; j < nv; j += kTopkThreads) n += tkeys[j] >= cand ? 1 : 0;
-      n = __reduce_add_sync(0xffffffffu, n);
+    // keys that reach c1, c2 and c3 (c1 <= c2 <= c3): counts of at most 24576 in 16 bits each
+    int turn = 0;
+    auto count = [&](unsigned long long c1, unsigned long long c2, unsigned long long c3) {
+      uint32_t lo = 0, hi = 0;
+      for (int j = t; j < nv; j += kTopkThreads) {
+        const unsigned long long k = tkeys[j];
+        lo += (k >= c1 ? 1u : 0u) + (k >= c2 ? 1u << 16 : 0u);
+        hi += k >= c3 ? 1u : 0u;
+      }
+      lo = __reduce_add_sync(0xffffffffu, lo);
+      hi = __reduce_add_sync(0xffffffffu, hi);
+      if (lane == 0) red[turn][warp] = static_cast<unsigned long long>(hi) << 32 | lo;
       __syncthreads();
-      if (lane == 0) red[warp] = n;
-      __syncthreads();
-      n = 0;
-      for (int i = 0; i < kTopkThreads / 32; ++i) n += red[i];
+      unsigned long long n = 0;
+#pragma unroll
+      for (int i = 0; i < WARPS; ++i) n += red[turn][i];
+      turn ^= 1;  // the sums of the call before this one may still be read
       return n;
     };
-    // the kk-th largest key, bit by bit; at_cut = keys that reach it
+    // the kk-th largest key, two bits a step; at_cut = keys that reach it
     unsigned long long cut = 0;
     int at_cut = nv;
-    for (int bit = 63; bit >= 0 && at_cut != kk; --bit) {
-      const unsigned long long cand = cut | (1ull << bit);
-      const int n = count(cand);
-      if (n >= kk) cut = cand, at_cut = n;
+    for (int bit = 62; bit >= 0 && at_cut != kk; bit -= 2) {
+      const unsigned long long one = 1ull << bit;
+      const unsigned long long n = count(cut | one, cut | (one << 1), cut | (one << 1) | one);
+      const int n1 = static_cast<int>(n & 0xffff), n2 = static_cast<int>(n >> 16 & 0xffff), n3 = static_cast<int>(n >> 32);
+      if (n3 >= kk) cut |= (one << 1) | one, at_cut = n3;
+      else if (n2 >= kk) cut |= one << 1, at_cut = n2;
+      else if (n1 >= kk) cut |= one, at_cut = n1;
     }
     // keys above the cut, and of those equal to it the first `ties`
     int ties = kk;
-    if (at_cut != kk) ties = kk - (cut == ~0ull ? 0 : count(cut + 1));
+    if (at_cut != kk) ties = kk - (cut == ~0ull ? 0 : static_cast<int>(count(cut + 1, cut + 1, cut + 1) & 0xffff));
     int base = 0, eq_base = 0;
     for (int j0 = 0; j0 < nv; j0 += kTopkThreads) {
       const int j = j0 + t;
@@ -338,15 +381,16 @@ __global__ void __launch_bounds__(kTopkThreads) block_pick_kernel(const TopkPara
       const bool gt = j < nv && (at_cut != kk ? k > cut : k >= cut);
       // counts of both kinds in the warps before this one, packed in one word
       const unsigned beq = __ballot_sync(0xffffffffu, eq), bgt = __ballot_sync(0xffffffffu, gt);
-      __syncthreads();
-      if (lane == 0) red[warp] = __popc(bgt) | (__popc(beq) << 16);
+      if (lane == 0) red[turn][warp] = __popc(bgt) | (__popc(beq) << 16);
       __syncthreads();
       int gt_before = 0, eq_before = 0, gt_all = 0, eq_all = 0;
-      for (int i = 0; i < kTopkThreads / 32; ++i) {
-        const int v = red[i];
+#pragma unroll
+      for (int i = 0; i < WARPS; ++i) {
+        const int v = static_cast<int>(red[turn][i]);
         if (i < warp) gt_before += v & 0xffff, eq_before += v >> 16;
         gt_all += v & 0xffff, eq_all += v >> 16;
       }
+      turn ^= 1;
       const unsigned lt = (1u << lane) - 1u;
       const int eq_rank = eq_base + eq_before + __popc(beq & lt);  // this key's place among the equal ones
       const int gt_rank = base + gt_before + __popc(bgt & lt);     // chosen keys above the cut before it
@@ -374,8 +418,26 @@ struct CacheWriteParams {
 
 constexpr int kCacheThreads = 256;
 
+// Four e4m3 values of x / scale: the rounded fp32 quotient, to the nearest e4m3.  With the rounded reciprocal
+// y of the scale at hand, q = RN(x y) and RN(q + RN(x - q scale) y) is the rounded quotient (P. Markstein,
+// Computation of elementary functions on the IBM RISC System/6000, 1990, for a q within a step of it; for
+// the quotients that occur here, 8-bit x by the fp32 rounding of an 8-bit number / 448, all mantissas are
+// checked on the CPU): two multiply-adds where a division is some ten instructions and one of the XU's.
+template <bool PLAIN>
+__device__ __forceinline__ unsigned quantise4(const float* x, float scale, float inv) {
+  float y[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float q = x[e] * inv;
+    y[e] = PLAIN ? fmaf(fmaf(-q, scale, x[e]), inv, q) : x[e] / scale;
+  }
+  const unsigned lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
+  const unsigned hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
 template <int HD>
-__global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheWriteParams p) {
+__global__ void __launch_bounds__(kCacheThreads, 4) cache_write_kernel(const CacheWriteParams p) {
   constexpr int CG = HD / 16;                       // 16-element pieces of a row
   constexpr int RG = kCacheThreads / CG;            // rows of one pass
   constexpr int NIT = 128 / RG;                     // passes over the largest block
@@ -401,14 +463,28 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheW
       u[i][0] = u[i][1] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
+  // |x| as 16-bit integers, two at a time; infinities and NaN, which lie above every number, are left
+  // out in a second look where there are any
+  unsigned pairs = 0;
 #pragma unroll
   for (int i = 0; i < NIT; ++i) {
     const unsigned* w = reinterpret_cast<const unsigned*>(u[i]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const unsigned a = w[e] & 0x7fffu, b = (w[e] >> 16) & 0x7fffu;
-      top = max(top, a < 0x7f80u ? a : 0u);
-      top = max(top, b < 0x7f80u ? b : 0u);
+    for (int e = 0; e < 8; ++e) pairs = __vmaxu2(pairs, w[e] & 0x7fff7fffu);
+  }
+  top = max(pairs & 0xffffu, pairs >> 16);
+  const bool special = top >= 0x7f80u;
+  if (special) {
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < NIT; ++i) {
+      const unsigned* w = reinterpret_cast<const unsigned*>(u[i]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const unsigned a = w[e] & 0x7fffu, b = (w[e] >> 16) & 0x7fffu;
+        top = max(top, a < 0x7f80u ? a : 0u);
+        top = max(top, b < 0x7f80u ? b : 0u);
+      }
     }
   }
   top = __reduce_max_sync(0xffffffffu, top);
@@ -418,46 +494,53 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheW
   for (int i = 0; i < WARPS; ++i) top = max(top, wmax[i]);
   const float amax = __uint_as_float(top << 16);
   const float scale = top == 0u ? 1.f : fmaxf(amax / 448.f, 7.8886090522101181e-31f);  // 2^-100
+  const float inv = 1.f / scale;
   const size_t blk = static_cast<size_t>(bh) * (p.cap / p.BK) + p.start / p.BK + j;
   if (t == 0) p.scale[which][blk] = scale;
   uint8_t* dst = p.Y[which] + (static_cast<size_t>(bh) * p.cap + p.start + static_cast<size_t>(j) * p.BK) * HD + c * 16;
-#pragma unroll
-  for (int i = 0; i < NIT; ++i) {
-    const int r = r0 + i * RG;
-    if (r < rows) {
-      float f[16];
-      unpack8(u[i][0], f);
-      unpack8(u[i][1], f + 8);
-      unsigned w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const unsigned lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * e] / scale, f[4 * e + 1] / scale), __NV_SATFINITE, __NV_E4M3);
-        const unsigned hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * e + 2] / scale, f[4 * e + 3] / scale), __NV_SATFINITE, __NV_E4M3);
-        w[e] = lo | (hi << 16);
-      }
-      *reinterpret_cast<uint4*>(dst + static_cast<size_t>(r) * HD) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  }
-  if (which == 0 && p.means != nullptr) {
-    // the block's mean key, of the values before rounding (fp64 sums as in block_means_kernel)
-    double acc[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) acc[e] = 0.0;
+  auto store = [&](auto plain) {
 #pragma unroll
     for (int i = 0; i < NIT; ++i) {
-      float f[16];
-      unpack8(u[i][0], f);
-      unpack8(u[i][1], f + 8);
+      const int r = r0 + i * RG;
+      if (r < rows) {
+        unsigned w[4];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[e] += static_cast<double>(f[e]);
+        for (int h = 0; h < 2; ++h) {
+          float f[8];
+          unpack8(u[i][h], f);
+          w[2 * h] = quantise4<decltype(plain)::value>(f, scale, inv);
+          w[2 * h + 1] = quantise4<decltype(plain)::value>(f + 4, scale, inv);
+        }
+        *reinterpret_cast<uint4*>(dst + static_cast<size_t>(r) * HD) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
+  };
+  // infinities and NaN, and scales so small that a remainder could underflow, are divided
+  if (!special && scale >= 8.2718061255302767e-25f) store(std::true_type{});  // 2^-80
+  else store(std::false_type{});
+  if (which == 0 && p.means != nullptr) {
+    // the block's mean key, of the values before rounding (fp64 sums as in block_means_kernel)
+    // eight columns at a time: the sums of sixteen would not fit beside the tile
 #pragma unroll
-    for (int o = CG; o < 32; o <<= 1)
+    for (int half = 0; half < 2; ++half) {
+      double acc[8];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
-    if (lane < CG)
+      for (int e = 0; e < 8; ++e) acc[e] = 0.0;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) wsum[warp][c * 16 + e] = acc[e];
+      for (int i = 0; i < NIT; ++i) {
+        float f[8];
+        unpack8(u[i][half], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += static_cast<double>(f[e]);
+      }
+#pragma unroll
+      for (int o = CG; o < 32; o <<= 1)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
+      if (lane < CG)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) wsum[warp][c * 16 + half * 8 + e] = acc[e];
+    }
     __syncthreads();
     if (t < HD) {
       double s = 0.0;

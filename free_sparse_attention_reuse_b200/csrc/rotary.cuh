@@ -21,7 +21,7 @@ namespace mcs {
 
 constexpr int kRotMaxAxes = 4;
 constexpr int kRotThreads = 256;
-constexpr int kRotMaxTokens = 16;  // tokens of a CTA
+constexpr int kRotRows = 4;  // rows that a group has in flight
 
 struct RotaryParams {
   const __nv_bfloat16* x[3];  // q, k, v (nullable k, v)
@@ -49,6 +49,13 @@ __device__ __forceinline__ void unpack8(const uint4& u, float* f) {
     f[2 * i + 1] = t.y;
   }
 }
+// 16 bytes that no one writes during the kernel; loads in a row stay in a row, so that all of them are in
+// flight before the first is used.
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 u;
+  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+  return u;
+}
 __device__ __forceinline__ uint4 pack8(const float* f) {
   return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                     pack_bf16x2(f[6], f[7]));
@@ -65,115 +72,127 @@ __device__ __forceinline__ void load_w8(const void* w, int bf16, size_t at, floa
   }
 }
 
-// One CTA: T consecutive tokens of one batch entry, all heads of q, k and v; the sines and cosines
-// of a token are made once and shared by all its rows.  HD/8 lanes hold a row, 8 elements each.
+// One CTA: T consecutive tokens of one batch entry.  HD / 8 lanes make a group and hold a row, 8 elements
+// each; a group keeps to one token, whose sines and cosines stay in its registers, and goes through its
+// heads (through a share of them where there are more groups than tokens), kRotRows rows in flight.
+// Bound: device memory; one row in flight and the sines in shared memory left it at 58 % of the copy rate.
 template <int HD, int NORM, bool HALVES>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
-  constexpr int LPR = HD / 8;            // lanes per row
-  constexpr int RPW = 32 / LPR;          // rows per warp and pass
-  constexpr int WARPS = kRotThreads / 32;
-  __shared__ float2 cs[kRotMaxTokens * (HD / 2)];
-  __shared__ float rs[2][kRotMaxTokens];
+  constexpr int LPR = HD / 8;                 // lanes of a group
+  constexpr int GROUPS = kRotThreads / LPR;   // 16 or 32
+  constexpr int PAIRS = HALVES ? 8 : 4;       // rotations that a lane's 8 elements need
+  __shared__ float part[2][GROUPS];
   const int b = blockIdx.x / p.tiles, n0 = (blockIdx.x - b * p.tiles) * p.T;
-  const int nt = min(p.T, p.N - n0);
-  const int warp = warp_id(), lane = lane_id();
-  const int c = lane % LPR, sub = lane / LPR;
+  const int group = threadIdx.x / LPR, c = threadIdx.x % LPR;
+  const int t = group % p.T, share = group / p.T, shares = GROUPS / p.T;
+  const bool live = n0 + t < p.N;
+  const int n = live ? n0 + t : p.N - 1;  // (idle groups follow along on the last token and store nothing)
 
-  for (int i = threadIdx.x; i < nt * p.half; i += kRotThreads) {
-    const int t = i / p.half, j = i - t * p.half;
-    const size_t at = (static_cast<size_t>(p.pos_batch ? b : 0) * p.N + n0 + t) * p.A + p.axis[j];
-    const double x = p.pos_float ? static_cast<double>(static_cast<const float*>(p.pos)[at])
-                                 : static_cast<double>(static_cast<const int32_t*>(p.pos)[at]);
-    const double a = x * p.turns[j];
-    float2 v;
-    sincospif(2.f * static_cast<float>(a - rint(a)), &v.y, &v.x);
-    cs[t * (HD / 2) + j] = v;
-  }
-  if (NORM == kNormToken) {
-    // 1 / rms of each token's whole q and k: one warp per (tensor, token)
-    for (int u = warp; u < 2 * nt; u += WARPS) {
-      const int s = u / nt, t = u - s * nt;
-      if (p.x[s] == nullptr) continue;
-      const __nv_bfloat16* row = p.x[s] + b * p.sb[s] + (n0 + t) * p.sn[s] + c * 8;
-      float ss = 0.f;
-      for (int h = sub; h < p.heads[s]; h += RPW) {
-        float f[8];
-        unpack8(*reinterpret_cast<const uint4*>(row + h * p.sh[s]), f);
+  // the partner elements of HALVES are the same 8 slots of the lane half / 8 further (or back)
+  const int hc = p.half / 8;
+  const bool lo = c < hc, hi = !lo && c < 2 * hc;
+  float2 cs[PAIRS];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (lane == 0) rs[s][t] = rsqrtf(ss / static_cast<float>(p.heads[s] * HD) + p.eps);
+  for (int i = 0; i < PAIRS; ++i) {
+    const int j = HALVES ? c * 8 + i - (hi ? p.half : 0) : c * 4 + i;
+    cs[i] = make_float2(1.f, 0.f);
+    if (HALVES ? lo || hi : j < p.half) {
+      const size_t at = (static_cast<size_t>(p.pos_batch ? b : 0) * p.N + n) * p.A + p.axis[j];
+      const double x = p.pos_float ? static_cast<double>(static_cast<const float*>(p.pos)[at])
+                                   : static_cast<double>(static_cast<const int32_t*>(p.pos)[at]);
+      const double a = x * p.turns[j];
+      sincospif(2.f * static_cast<float>(a - rint(a)), &cs[i].y, &cs[i].x);
     }
   }
-  __syncthreads();
 
+  float rs[2] = {1.f, 1.f};
+  if (NORM == kNormToken) {
+    // 1 / rms of the token's whole q and k
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      float ss = 0.f;
+      if (p.x[s] != nullptr) {
+        const __nv_bfloat16* row = p.x[s] + b * p.sb[s] + n * p.sn[s] + c * 8;
+#pragma unroll 8
+        for (int h = share; h < p.heads[s]; h += shares) {
+          float f[8];
+          unpack8(*reinterpret_cast<const uint4*>(row + h * p.sh[s]), f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
+        }
+      }
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (c == 0) part[s][group] = ss;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      float ss = 0.f;
+      for (int i = 0; i < shares; ++i) ss += part[s][i * p.T + t];
+      rs[s] = rsqrtf(ss / static_cast<float>(p.heads[s] * HD) + p.eps);
+    }
+  }
+
+#pragma unroll
   for (int s = 0; s < 3; ++s) {
     if (p.x[s] == nullptr) continue;
-    const int rows = p.heads[s] * nt;  // head-major, so that a head's tokens are written together
-    for (int r0 = warp * RPW; r0 < rows; r0 += WARPS * RPW) {
-      const int r = r0 + sub;
-      const bool live = r < rows;
-      const int h = live ? r / nt : 0, t = live ? r - h * nt : 0;
-      uint4 u = make_uint4(0u, 0u, 0u, 0u);
-      if (live)
-        u = *reinterpret_cast<const uint4*>(p.x[s] + b * p.sb[s] + (n0 + t) * p.sn[s] + h * p.sh[s] + c * 8);
-      if (s < 2) {
-        float f[8];
-        unpack8(u, f);
-        if (NORM != kNormNone) {
-          float k;
-          if (NORM == kNormHead) {
-            float ss = 0.f;
+    const __nv_bfloat16* src = p.x[s] + b * p.sb[s] + n * p.sn[s] + c * 8;
+    __nv_bfloat16* dst = p.y[s] + (static_cast<size_t>(b) * p.heads[s] * p.N + n) * HD + c * 8;
+    const size_t step = static_cast<size_t>(p.N) * HD;
+    float w[8];
+    if (s < 2) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
+      for (int i = 0; i < 8; ++i) w[i] = 1.f;
+      if (NORM == kNormHead && p.w[s] != nullptr) load_w8(p.w[s], p.w_bf16, c * 8, w);
+    }
+    for (int h0 = share; h0 < p.heads[s]; h0 += shares * kRotRows) {
+      uint4 u[kRotRows];
 #pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            k = rsqrtf(ss * (1.f / HD) + p.eps);
-          } else {
-            k = rs[s][t];
-          }
-          if (p.w[s] != nullptr) {
-            float w[8];
-            load_w8(p.w[s], p.w_bf16, (NORM == kNormToken ? static_cast<size_t>(h) * HD : 0) + c * 8, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = f[i] * k * w[i];
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] *= k;
-          }
-        }
-        const float2* ct = cs + t * (HD / 2);
-        if (!HALVES) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = c * 4 + i;
-            if (j < p.half) {
-              const float2 v = ct[j];
-              const float x1 = f[2 * i], x2 = f[2 * i + 1];
-              f[2 * i] = x1 * v.x - x2 * v.y;
-              f[2 * i + 1] = x1 * v.y + x2 * v.x;
-            }
-          }
-        } else {
-          // the partner elements are the same 8 slots of the lane half/8 further (or back)
-          const int hc = p.half / 8;
-          const bool lo = c < hc, hi = !lo && c < 2 * hc;
-          const int src = lane + (lo ? hc : hi ? -hc : 0);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float o = __shfl_sync(0xffffffffu, f[i], src);
-            if (lo || hi) {
-              const float2 v = ct[c * 8 + i - (hi ? p.half : 0)];
-              f[i] = lo ? f[i] * v.x - o * v.y : o * v.y + f[i] * v.x;
-            }
-          }
-        }
-        u = pack8(f);
+      for (int k = 0; k < kRotRows; ++k) {
+        const int h = h0 + k * shares;
+        u[k] = h < p.heads[s] ? load16(src + h * p.sh[s]) : make_uint4(0u, 0u, 0u, 0u);
       }
-      if (live)
-        *reinterpret_cast<uint4*>(p.y[s] + ((static_cast<size_t>(b) * p.heads[s] + h) * p.N + n0 + t) * HD + c * 8) = u;
+#pragma unroll
+      for (int k = 0; k < kRotRows; ++k) {
+        const int h = h0 + k * shares;
+        if (s < 2) {
+          float f[8];
+          unpack8(u[k], f);
+          if (NORM != kNormNone) {
+            float r = rs[s];
+            if (NORM == kNormHead) {
+              float ss = 0.f;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
+#pragma unroll
+              for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+              r = rsqrtf(ss * (1.f / HD) + p.eps);
+            } else if (p.w[s] != nullptr) {
+              load_w8(p.w[s], p.w_bf16, static_cast<size_t>(min(h, p.heads[s] - 1)) * HD + c * 8, w);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = f[i] * r * w[i];
+          }
+          if (!HALVES) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float x1 = f[2 * i], x2 = f[2 * i + 1];
+              f[2 * i] = x1 * cs[i].x - x2 * cs[i].y;
+              f[2 * i + 1] = x1 * cs[i].y + x2 * cs[i].x;
+            }
+          } else {
+            const int from = static_cast<int>(lane_id()) + (lo ? hc : hi ? -hc : 0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float o = __shfl_sync(0xffffffffu, f[i], from);
+              if (lo || hi) f[i] = lo ? f[i] * cs[i].x - o * cs[i].y : o * cs[i].y + f[i] * cs[i].x;
+            }
+          }
+          u[k] = pack8(f);
+        }
+        if (live && h < p.heads[s]) *reinterpret_cast<uint4*>(dst + h * step) = u[k];
+      }
     }
   }
 }
