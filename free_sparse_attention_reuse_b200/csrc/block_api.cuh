@@ -18,6 +18,23 @@ mcs_status check_block_shape(const mcs_block_shape& s) {
     return MCS_ERR_SHAPE;
   return MCS_OK;
 }
+// Launch as a dependent of the kernel before it on the stream: its CTAs may start while that one still
+// runs, and wait for its results where they need them (wait_for_results).
+template <typename... Params, typename... Args>
+void launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 bool block_rows_ok(int BK) { return BK == 32 || BK == 64 || BK == 128; }
 bool query_rows_ok(int C) { return C == 1 || C == 16 || C == 64 || C == 128; }
 
@@ -101,8 +118,8 @@ template <int HD>
 void join_parts(const BlockAttnParams& p, cudaStream_t st) {
   if (p.splits == 1) return;
   const long long rows = static_cast<long long>(p.B) * p.H * p.Nq;
-  constexpr int per = 256 / (HD / 4);
-  block_join_kernel<HD><<<static_cast<unsigned>((rows + per - 1) / per), 256, 0, st>>>(p);
+  constexpr int per = 256 / (HD / 4) / kJoinGroups;
+  launch_dependent(block_join_kernel<HD>, dim3(static_cast<unsigned>((rows + per - 1) / per)), 256, 0, st, p);
 }
 
 template <int HD>
@@ -148,7 +165,7 @@ void launch_means(int d, const __nv_bfloat16* X, const int32_t* len, float* mean
   p.BK = BK;
   p.nb = (N + BK - 1) / BK;
   p.blocks = static_cast<long long>(B) * H * p.nb;
-  const unsigned grid = static_cast<unsigned>((p.blocks + kMeansThreads / 32 - 1) / (kMeansThreads / 32));
+  const unsigned grid = static_cast<unsigned>(p.blocks);
   if (d == 64) block_means_kernel<64><<<grid, kMeansThreads, 0, st>>>(p);
   else block_means_kernel<128><<<grid, kMeansThreads, 0, st>>>(p);
 }
@@ -178,20 +195,27 @@ TopkPlan plan_topk(const mcs_block_shape& s, int C, int BK) {
 
 template <int HD>
 void launch_topk(const TopkParams& p, int kvs, cudaStream_t st) {
+  const unsigned few = static_cast<unsigned>((p.nb + kFewBlocks - 1) / kFewBlocks);
   const unsigned tiles = static_cast<unsigned>((p.nb + kScoreTile - 1) / kScoreTile);
-  static_assert(kScoreTile == kFewBlocks, "one grid for both forms");
-  // few rows: the tile form would spend its 64 rows on them (3 rows, 64 key heads: 30 us against 6)
-  if (p.mc <= kFewRows) block_score_few_kernel<HD><<<dim3(tiles, 1, kvs), 128, 0, st>>>(p);
-  else block_score_kernel<HD><<<dim3(tiles, (p.mc + kScoreTile - 1) / kScoreTile, kvs), kScoreThreads, 0, st>>>(p);
+  const unsigned mtiles = static_cast<unsigned>((p.mc + kScoreTile - 1) / kScoreTile);
+  // few rows: the tile form would spend its 64 rows on them (3 rows, 64 key heads: 30 us against 8)
+  const bool first = p.qbar == nullptr;  // nothing of this call runs before it
+  if (p.mc <= kFewRows) {
+    if (first) block_score_few_kernel<HD><<<dim3(few, 1, kvs), 128, 0, st>>>(p);
+    else launch_dependent(block_score_few_kernel<HD>, dim3(few, 1, kvs), 128, 0, st, p);
+  } else {
+    if (first) block_score_kernel<HD><<<dim3(tiles, mtiles, kvs), kScoreThreads, 0, st>>>(p);
+    else launch_dependent(block_score_kernel<HD>, dim3(tiles, mtiles, kvs), kScoreThreads, 0, st, p);
+  }
   const long long rows = static_cast<long long>(kvs) * p.mc;
   const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
   const bool warps = rows >= kPickWarpRows;  // enough of them to fill the GPU with a warp each
-  if (warps && p.nb <= 8 * 32) block_pick_warp_kernel<8><<<grid, 128, 0, st>>>(p, rows);
-  else if (warps && p.nb <= 16 * 32) block_pick_warp_kernel<16><<<grid, 128, 0, st>>>(p, rows);
-  else if (warps && p.nb <= 32 * 32) block_pick_warp_kernel<32><<<grid, 128, 0, st>>>(p, rows);
+  if (warps && p.nb <= 8 * 32) launch_dependent(block_pick_warp_kernel<8>, grid, 128, 0, st, p, rows);
+  else if (warps && p.nb <= 16 * 32) launch_dependent(block_pick_warp_kernel<16>, grid, 128, 0, st, p, rows);
+  else if (warps && p.nb <= 32 * 32) launch_dependent(block_pick_warp_kernel<32>, grid, 128, 0, st, p, rows);
   else
-    block_pick_kernel<<<static_cast<unsigned>(std::min<long long>(rows, 4096)), kTopkThreads,
-                        static_cast<size_t>(p.nb) * 8, st>>>(p, rows);
+    launch_dependent(block_pick_kernel, static_cast<unsigned>(std::min<long long>(rows, 4096)), kTopkThreads,
+                     static_cast<size_t>(p.nb) * 8, st, p, rows);
 }
 
 template <int HD, int NORM>

@@ -914,40 +914,63 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 }
 
 // ---------------------------------------------------------------------------------- splits joined
-// out = sum_s 2^(l_s - l) o_s (+ R), l = log2 sum_s 2^l_s over the parts of a row's keys; HD / 4 lanes a row.
+// out = sum_s 2^(l_s - l) o_s (+ R), l = log2 sum_s 2^l_s over the parts of a row's keys.  A CTA takes a few
+// rows, HD / 4 lanes a row, and shares each row's parts out over its groups of lanes.
+constexpr int kJoinGroups = 4;  // groups to a row
+
 template <int HD>
 __global__ void __launch_bounds__(256) block_join_kernel(const BlockAttnParams p) {
-  constexpr int LPR = HD / 4, RPB = 256 / LPR;
+  constexpr int LPR = HD / 4, RPB = 256 / LPR / kJoinGroups;  // lanes to a row, rows of a CTA
+  __shared__ float sm_m[kJoinGroups][RPB], sm_l[kJoinGroups][RPB];
+  __shared__ __align__(16) float4 sm_o[kJoinGroups][RPB][LPR];
   const long long rows = static_cast<long long>(p.B) * p.H * p.Nq;
-  const long long row = static_cast<long long>(blockIdx.x) * RPB + threadIdx.x / LPR;
-  const int c = (threadIdx.x % LPR) * 4;
-  if (row >= rows) return;
-  float m = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, p.plse[s * rows + row]);
-  const float mz = m == -INFINITY ? 0.f : m;
-  float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < p.splits; ++s) {
-    const float w = exp2f(p.plse[s * rows + row] - mz);
-    const float4 v = *reinterpret_cast<const float4*>(p.part + (s * rows + row) * HD + c);
-    l += w;
-    o[0] = fmaf(w, v.x, o[0]);
-    o[1] = fmaf(w, v.y, o[1]);
-    o[2] = fmaf(w, v.z, o[2]);
-    o[3] = fmaf(w, v.w, o[3]);
+  const int lane = threadIdx.x % LPR, r = threadIdx.x / LPR % RPB, grp = threadIdx.x / LPR / RPB;
+  const long long row = static_cast<long long>(blockIdx.x) * RPB + r;
+  const bool live = row < rows;
+  wait_for_results();
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (live) {
+#pragma unroll 4
+    for (int s = grp; s < p.splits; s += kJoinGroups) {
+      const float x = p.plse[s * rows + row];
+      const float4 v = *reinterpret_cast<const float4*>(p.part + (s * rows + row) * HD + lane * 4);
+      const float mn = fmaxf(m, x), ref = mn == -INFINITY ? 0.f : mn;
+      const float a = exp2f(m - ref), w = exp2f(x - ref);
+      m = mn;
+      l = fmaf(l, a, w);
+      o = make_float4(fmaf(w, v.x, o.x * a), fmaf(w, v.y, o.y * a), fmaf(w, v.z, o.z * a), fmaf(w, v.w, o.w * a));
+    }
+  }
+  if (lane == 0) sm_m[grp][r] = m, sm_l[grp][r] = l;
+  sm_o[grp][r][lane] = o;
+  __syncthreads();
+  if (grp != 0 || !live) return;
+#pragma unroll
+  for (int i = 1; i < kJoinGroups; ++i) m = fmaxf(m, sm_m[i][r]);
+  const float ref = m == -INFINITY ? 0.f : m;
+  float f[4] = {0.f, 0.f, 0.f, 0.f};
+  l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kJoinGroups; ++i) {
+    const float w = exp2f(sm_m[i][r] - ref);
+    const float4 v = sm_o[i][r][lane];
+    l = fmaf(w, sm_l[i][r], l);
+    f[0] = fmaf(w, v.x, f[0]), f[1] = fmaf(w, v.y, f[1]), f[2] = fmaf(w, v.z, f[2]), f[3] = fmaf(w, v.w, f[3]);
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  float r[4] = {0.f, 0.f, 0.f, 0.f};
+  float add[4] = {0.f, 0.f, 0.f, 0.f};
   if (p.R != nullptr) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p.R + row * HD + c);
+    const uint2 u = *reinterpret_cast<const uint2*>(p.R + row * HD + lane * 4);
     const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
     const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-    r[0] = a.x, r[1] = a.y, r[2] = b.x, r[3] = b.y;
+    add[0] = a.x, add[1] = a.y, add[2] = b.x, add[3] = b.y;
   }
   uint2 w;
-  w.x = pack_bf16x2(fmaf(o[0], inv, r[0]), fmaf(o[1], inv, r[1]));
-  w.y = pack_bf16x2(fmaf(o[2], inv, r[2]), fmaf(o[3], inv, r[3]));
-  *reinterpret_cast<uint2*>(p.out + row * HD + c) = w;
-  if (p.lse != nullptr && c == 0) p.lse[row] = l == 0.f ? -INFINITY : (mz + log2f(l)) * 0.69314718055994531f;
+  w.x = pack_bf16x2(fmaf(f[0], inv, add[0]), fmaf(f[1], inv, add[1]));
+  w.y = pack_bf16x2(fmaf(f[2], inv, add[2]), fmaf(f[3], inv, add[3]));
+  *reinterpret_cast<uint2*>(p.out + row * HD + lane * 4) = w;
+  if (p.lse != nullptr && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace mcs

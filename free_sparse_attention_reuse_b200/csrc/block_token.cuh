@@ -53,6 +53,7 @@ __global__ void __launch_bounds__(kTokenWarps * 32, RT == 8 && HD == 64 ? 3 : 2)
   __shared__ __align__(16) float sm_o[kTokenWarps][RT][HD];
   __shared__ int s_end;
 
+  let_dependents_start();
   const int warp = warp_id(), lane = lane_id(), g = lane >> 2, t = lane & 3;
   const int unit = blockIdx.x;
   const int sp = unit % p.splits, tu = unit / p.splits;

@@ -36,13 +36,16 @@ struct MeansParams {
 
 constexpr int kMeansThreads = 128;
 
+// One CTA a block, its warps a share of the rows each.  Bound: device memory, with the widening to fp64 (XU)
+// at two thirds of that time; a warp a block left a last wave of few CTAs (46 us against 36 for 198 MB).
 template <int HD>
 __global__ void __launch_bounds__(kMeansThreads) block_means_kernel(const MeansParams p) {
-  constexpr int LPR = HD / 8, RPW = 32 / LPR;
-  const int lane = lane_id(), c = lane % LPR, sub = lane / LPR;
-  const long long blk = static_cast<long long>(blockIdx.x) * (kMeansThreads / 32) + warp_id();
-  if (blk >= p.blocks) return;
-  const long long bh = blk / p.nb;
+  constexpr int LPR = HD / 8, RPP = kMeansThreads / LPR;  // lanes of a row, rows of a pass
+  constexpr int WARPS = kMeansThreads / 32;
+  __shared__ double sums[WARPS][HD];
+  let_dependents_start();
+  const int t = threadIdx.x, lane = lane_id(), c = t % LPR;
+  const long long blk = blockIdx.x, bh = blk / p.nb;
   const int j = static_cast<int>(blk - bh * p.nb);
   const int n = min(p.BK, valid_rows(p.len, static_cast<int>(bh / p.H), p.N) - j * p.BK);
   const __nv_bfloat16* row = p.X + (static_cast<size_t>(bh) * p.N + static_cast<size_t>(j) * p.BK) * HD + c * 8;
@@ -55,26 +58,28 @@ __global__ void __launch_bounds__(kMeansThreads) block_means_kernel(const MeansP
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] += static_cast<double>(f[i]);
   };
-  int r = sub;
-  for (; r + 7 * RPW < n; r += 8 * RPW) {  // eight rows in flight
+  int r = t / LPR;
+  for (; r + 7 * RPP < n; r += 8 * RPP) {  // eight rows in flight
     uint4 u[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) u[k] = load16(row + static_cast<size_t>(r + k * RPW) * HD);
+    for (int k = 0; k < 8; ++k) u[k] = load16(row + static_cast<size_t>(r + k * RPP) * HD);
 #pragma unroll
     for (int k = 0; k < 8; ++k) add(u[k]);
   }
-  for (; r < n; r += RPW) add(load16(row + static_cast<size_t>(r) * HD));
+  for (; r < n; r += RPP) add(load16(row + static_cast<size_t>(r) * HD));
 #pragma unroll
   for (int o = LPR; o < 32; o <<= 1)
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-  if (sub == 0) {
-    float f[8];
+  if (lane < LPR)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = n > 0 ? static_cast<float>(acc[i] / static_cast<double>(n)) : 0.f;
-    float4* out = reinterpret_cast<float4*>(p.means + static_cast<size_t>(blk) * HD + c * 8);
-    out[0] = make_float4(f[0], f[1], f[2], f[3]);
-    out[1] = make_float4(f[4], f[5], f[6], f[7]);
+    for (int i = 0; i < 8; ++i) sums[warp_id()][c * 8 + i] = acc[i];
+  __syncthreads();
+  for (int e = t; e < HD; e += kMeansThreads) {
+    double s = 0.0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) s += sums[w][e];
+    p.means[static_cast<size_t>(blk) * HD + e] = n > 0 ? static_cast<float>(s / static_cast<double>(n)) : 0.f;
   }
 }
 
@@ -119,6 +124,8 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const TopkPa
   const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
   const int kv = p.kv0 + blockIdx.z, m0 = blockIdx.y * kScoreTile, j0 = blockIdx.x * kScoreTile;
   const int nv = candidate_blocks(p, kv);
+  let_dependents_start();
+  wait_for_results();  // the mean query rows (in every CTA: a grid that ends has seen the one before it end)
   if (j0 >= nv) return;
   const size_t row0 = static_cast<size_t>(kv) * p.M + p.m0 + m0;
   const int rows = p.mc - m0;
@@ -194,7 +201,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const TopkPa
 
 // At most kFewRows rows (one token): every mean is read once, eight lanes to a block, the rows in shared
 // memory.  Bound: reading the means (33.5 MB for 64 key heads of 1024 blocks of 128: 5 us).
-constexpr int kFewRows = 4, kFewBlocks = 64;  // rows; blocks a CTA of four warps takes
+constexpr int kFewRows = 4, kFewBlocks = 32;  // rows; blocks a CTA of four warps takes
 
 template <int HD>
 __global__ void __launch_bounds__(128) block_score_few_kernel(const TopkParams p) {
@@ -204,43 +211,53 @@ __global__ void __launch_bounds__(128) block_score_few_kernel(const TopkParams p
   const int kv = p.kv0 + blockIdx.z;
   const int nv = candidate_blocks(p, kv);
   const int j0 = blockIdx.x * kFewBlocks + warp_id() * (kFewBlocks / 4);
+  let_dependents_start();
+  wait_for_results();  // the mean query rows
+  if (static_cast<int>(blockIdx.x) * kFewBlocks >= nv) return;
   constexpr int IT = kFewBlocks / 16;
   float4 v[IT][CH];
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
-    const int j = j0 + i * 4 + sub;
+    const int j = min(j0 + i * 4 + sub, p.nb - 1);
 #pragma unroll
     for (int h = 0; h < CH; ++h)
-      v[i][h] = j < nv ? *reinterpret_cast<const float4*>(p.means + (static_cast<size_t>(kv) * p.nb + j) * HD + h * 32 + c * 4)
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[i][h] = *reinterpret_cast<const float4*>(p.means + (static_cast<size_t>(kv) * p.nb + j) * HD + h * 32 + c * 4);
   }
-  for (int i = threadIdx.x; i < p.mc * HD; i += 128) {
+  for (int i = threadIdx.x; i < kFewRows * HD; i += 128) {
     const int r = i / HD, e = i - r * HD;
     const size_t at = (static_cast<size_t>(kv) * p.M + p.m0 + r) * HD + e;
-    q[r][e] = p.qbar != nullptr ? static_cast<double>(p.qbar[at]) : static_cast<double>(__bfloat162float(p.Q[at]));
+    double x = 0.0;
+    if (r < p.mc) x = p.qbar != nullptr ? static_cast<double>(p.qbar[at]) : static_cast<double>(__bfloat162float(p.Q[at]));
+    q[r][e] = x;
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
     const int j = j0 + i * 4 + sub;
-    double x[CH * 4];
+    double s[kFewRows];  // side by side, so that their chains of sums overlap
 #pragma unroll
-    for (int h = 0; h < CH; ++h) x[4 * h] = v[i][h].x, x[4 * h + 1] = v[i][h].y, x[4 * h + 2] = v[i][h].z, x[4 * h + 3] = v[i][h].w;
-    for (int r = 0; r < p.mc; ++r) {
-      double s = 0.0;
+    for (int r = 0; r < kFewRows; ++r) s[r] = 0.0;
 #pragma unroll
-      for (int h = 0; h < CH; ++h) {
+    for (int h = 0; h < CH; ++h) {
+      const double x0 = v[i][h].x, x1 = v[i][h].y, x2 = v[i][h].z, x3 = v[i][h].w;
+#pragma unroll
+      for (int r = 0; r < kFewRows; ++r) {
         const double2 y = *reinterpret_cast<const double2*>(&q[r][h * 32 + c * 4]);
         const double2 z = *reinterpret_cast<const double2*>(&q[r][h * 32 + c * 4 + 2]);
-        s = fma(x[4 * h], y.x, s);
-        s = fma(x[4 * h + 1], y.y, s);
-        s = fma(x[4 * h + 2], z.x, s);
-        s = fma(x[4 * h + 3], z.y, s);
+        s[r] = fma(x0, y.x, s[r]);
+        s[r] = fma(x1, y.y, s[r]);
+        s[r] = fma(x2, z.x, s[r]);
+        s[r] = fma(x3, z.y, s[r]);
       }
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (c == 0 && j < nv) p.keys[(static_cast<size_t>(blockIdx.z) * p.mc + r) * p.nb + j] = score_key(s);
     }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+      for (int r = 0; r < kFewRows; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
+    if (c == 0 && j < nv)
+#pragma unroll
+      for (int r = 0; r < kFewRows; ++r)
+        if (r < p.mc) p.keys[(static_cast<size_t>(blockIdx.z) * p.mc + r) * p.nb + j] = score_key(s[r]);
   }
 }
 
@@ -253,6 +270,7 @@ __global__ void __launch_bounds__(128) block_pick_warp_kernel(const TopkParams p
   const int lane = lane_id();
   const int kv = p.kv0 + static_cast<int>(r / p.mc);
   const int nv = candidate_blocks(p, kv), kk = min(p.kb, nv);
+  wait_for_results();  // the keys
   const unsigned long long* keys = p.keys + static_cast<size_t>(r) * p.nb;
   int32_t* out = p.blocks + (static_cast<size_t>(kv) * p.M + p.m0 + static_cast<int>(r % p.mc)) * p.kb;
   uint32_t w[KPL];  // high words, then the low words of the keys at the cut
@@ -332,6 +350,7 @@ __global__ void __launch_bounds__(kTopkThreads) block_pick_kernel(const TopkPara
   constexpr int WARPS = kTopkThreads / 32;
   __shared__ unsigned long long red[2][WARPS];
   const int t = threadIdx.x, lane = lane_id(), warp = warp_id();
+  wait_for_results();  // the keys
   for (long long r = blockIdx.x; r < rows; r += gridDim.x) {
     const int kv = p.kv0 + static_cast<int>(r / p.mc);
     const int nv = candidate_blocks(p, kv), kk = min(p.kb, nv);

@@ -49,6 +49,11 @@ __device__ __forceinline__ void unpack8(const uint4& u, float* f) {
     f[2 * i + 1] = t.y;
   }
 }
+// A kernel launched as another's dependent starts while that one still runs and waits here for its results
+// (at once where it was launched the plain way); the other lets it start with let_dependents_start.
+__device__ __forceinline__ void wait_for_results() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // 16 bytes that no one writes during the kernel; loads in a row stay in a row, so that all of them are in
 // flight before the first is used.
 __device__ __forceinline__ uint4 load16(const void* p) {
