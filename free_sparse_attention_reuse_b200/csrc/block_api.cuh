@@ -49,6 +49,12 @@ bool block_attn_attrs() {
          cudaFuncGetAttributes(&fa, block_attn_kernel<HD, KV8, PAIR>) == cudaSuccess &&
          static_cast<long long>(fa.numRegs) * kAttnThreads == 65536;
 }
+template <int HD, bool KV8>
+bool block_token_attrs() {
+  constexpr int bytes = TokenSmem<HD, KV8>::BYTES;
+  return cudaFuncSetAttribute(block_token_kernel<HD, KV8, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess &&
+         cudaFuncSetAttribute(block_token_kernel<HD, KV8, 16>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+}
 mcs_status block_device(DeviceInfo** out) {
   mcs_status e = current_device(out);
   if (e != MCS_OK) return e;
@@ -56,7 +62,8 @@ mcs_status block_device(DeviceInfo** out) {
   if (!(*out)->block_attrs_set) {
     const int topk = kTopkMaxBlocks * 8;
     if (cudaFuncSetAttribute(block_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, topk) != cudaSuccess ||
-        !block_attn_attrs<64, false, false>() || !block_attn_attrs<64, false, true>() ||
+        !block_token_attrs<64, false>() || !block_token_attrs<64, true>() || !block_token_attrs<128, false>() ||
+        !block_token_attrs<128, true>() || !block_attn_attrs<64, false, false>() || !block_attn_attrs<64, false, true>() ||
         !block_attn_attrs<64, true, false>() || !block_attn_attrs<64, true, true>() ||
         !block_attn_attrs<128, false, false>() || !block_attn_attrs<128, false, true>() ||
         !block_attn_attrs<128, true, false>() || !block_attn_attrs<128, true, true>())
@@ -126,10 +133,12 @@ template <int HD>
 mcs_status run_block_token(const BlockAttnParams& p, bool kv8, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(static_cast<long long>(p.B) * p.H * p.GQ * p.splits);
   const bool few = std::min(p.C, p.Nq) <= 8;
-  if (kv8 && few) block_token_kernel<HD, true, 8><<<grid, kTokenWarps * 32, 0, st>>>(p);
-  else if (kv8) block_token_kernel<HD, true, 16><<<grid, kTokenWarps * 32, 0, st>>>(p);
-  else if (few) block_token_kernel<HD, false, 8><<<grid, kTokenWarps * 32, 0, st>>>(p);
-  else block_token_kernel<HD, false, 16><<<grid, kTokenWarps * 32, 0, st>>>(p);
+  constexpr unsigned threads = kTokenWarps * 32;
+  constexpr size_t b16 = TokenSmem<HD, false>::BYTES, b8 = TokenSmem<HD, true>::BYTES;
+  if (kv8 && few) block_token_kernel<HD, true, 8><<<grid, threads, b8, st>>>(p);
+  else if (kv8) block_token_kernel<HD, true, 16><<<grid, threads, b8, st>>>(p);
+  else if (few) block_token_kernel<HD, false, 8><<<grid, threads, b16, st>>>(p);
+  else block_token_kernel<HD, false, 16><<<grid, threads, b16, st>>>(p);
   join_parts<HD>(p, st);
   return launch_status();
 }

@@ -1,17 +1,17 @@
 // Attention over listed key blocks for few query rows (one token, one token of several heads, up to 16 rows
-// of a list): the keys and values are read once from memory and little else happens, so nothing is
-// staged in shared memory.  Every warp streams runs of keys straight into the registers of mma.sync
-// fragments (16 rows, of which as many count as there are):
+// of a list): the keys and values are read once from memory and little else happens.  A list's runs of 16 or
+// 32 keys, which lie one behind the other in memory, are shared out over four warps; each warp keeps a
+// ring of runs in flight with bulk copies (its loads straight into registers reached 3.1 TB/s: too few
+// bytes under way for the registers they took) and multiplies with mma.sync (16 rows, of which as
+// many count as there are):
 //
 //   S = Q K^T   contraction over d in an order of our choosing: a lane's 16 consecutive bytes of a key row
 //               are its B fragments of two (bf16) or four (e4m3) k steps, Q's fragments follow suit;
 //   O = P V     the columns in an order of our choosing: a lane's 16 bytes of four value rows, two rows
 //               interleaved, are its B fragments of eight (16) column tiles.
 //
-// A lane loads 16 bytes at a time and a warp's load covers whole 32-byte sectors; a run's values are
-// loaded while its logits are formed, the next run's keys while the softmax runs.  Running maximum and
-// sum per row, in fp32 and base 2; a CTA's four warps are merged through shared memory, the CTAs of a
-// split list by block_join_kernel.  Bound: device memory.
+// Running maximum and sum per row, in fp32 and base 2; a CTA's four warps are merged through shared memory,
+// the CTAs of a split list by block_join_kernel.  Bound: device memory.
 #pragma once
 
 #include "block_attn.cuh"
@@ -20,38 +20,106 @@ namespace mcs {
 
 constexpr int kTokenWarps = 4;
 
+// C += A B for 16 rows (F16: fp16 operands, else bf16), and for at most 8: the upper half of A is zero
+// and that of the result is dropped.
+template <bool F16>
 __device__ __forceinline__ void mma_16816(float& c0, float& c1, float& c2, float& c3, uint32_t a0, uint32_t a1,
                                           uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c0), "+f"(c1), "+f"(c2), "+f"(c3)
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if constexpr (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c0), "+f"(c1), "+f"(c2), "+f"(c3)
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c0), "+f"(c1), "+f"(c2), "+f"(c3)
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// The same for at most 8 rows: the upper half of A is zero and that of the result is dropped.
+template <bool F16>
 __device__ __forceinline__ void mma_8816(float& c0, float& c1, uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
   [[maybe_unused]] float x, y;
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, {%0,%1,%9,%9};"
-      : "+f"(c0), "+f"(c1), "=f"(x), "=f"(y)
-      : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1), "f"(0.f));
+  if constexpr (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, {%0,%1,%9,%9};"
+        : "+f"(c0), "+f"(c1), "=f"(x), "=f"(y)
+        : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, {%0,%1,%9,%9};"
+        : "+f"(c0), "+f"(c1), "=f"(x), "=f"(y)
+        : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1), "f"(0.f));
 }
-// Two e4m3 values (low 16 bits) to bf16, exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16(uint32_t x) {
-  const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(x & 0xffffu), __NV_E4M3)));
-  return pack_bf16x2(f.x, f.y);
+// Four e4m3 values to fp16, exact: the lower two and the upper two.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// A row of Q as fp16 fragments: times the power of two that brings its largest element into [2^14, 2^15),
+// which `unscale` takes back.  Exact for elements down to 2^-28 of the largest, off by at most 2^-40 of
+// it below.  (A row with infinities or NaN gives NaN either way.)
+template <int N>
+__device__ __forceinline__ float q_to_f16(uint32_t* q) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&q[i]));
+    top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+  }
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  // exponent of the largest element, kept where both powers of two are normal numbers
+  const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 20), 254) - 127;
+  const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&q[i]));
+    q[i] = pack_f16x2(f.x * up, f.y * up);
+  }
+  return __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
 }
 
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 u;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(a));
+  return u;
+}
+
+template <int HD, bool KV8>
+struct TokenSmem {
+  static constexpr int KC = KV8 || HD == 64 ? 32 : 16;             // keys of a run
+  static constexpr uint32_t ROW = HD * (KV8 ? 1 : 2);              // bytes of a row
+  static constexpr uint32_t RUN = KC * ROW;                        // of a run's keys, or values
+  static constexpr int RING = 24576 / (2 * RUN);                   // runs that a warp has in hand: 3 or 6
+  static constexpr uint32_t WARP = RING * 2 * RUN;                 // 24 KB
+  static constexpr uint32_t BYTES = kTokenWarps * WARP;            // the warps' results lie over it at the end
+  static_assert(kTokenWarps * 16 * HD * 4 <= BYTES, "results fit");
+};
+
 template <int HD, bool KV8, int RT>
-__global__ void __launch_bounds__(kTokenWarps * 32, RT == 8 && HD == 64 ? 3 : 2) block_token_kernel(const BlockAttnParams p) {
-  constexpr int KC = KV8 || HD == 64 ? 32 : 16;  // keys of a run
+__global__ void __launch_bounds__(kTokenWarps * 32, 2) block_token_kernel(const BlockAttnParams p) {
+  using L = TokenSmem<HD, KV8>;
+  constexpr int KC = L::KC, RING = L::RING;
   constexpr int NT = KC / 8;                     // key tiles
   constexpr int LB = HD * (KV8 ? 1 : 2) / 64;    // 16-byte loads of a lane per key row (4 lanes a row)
   constexpr int KS = KV8 ? 4 : 2;                // k steps that such a load feeds
   constexpr int VC = KV8 ? HD / 8 : 8;           // columns that a lane loads of a value row at once
   constexpr int VH = HD / (8 * VC);              // such loads per value row
   constexpr int WIDE = RT == 16;
-  using Val = typename std::conditional<VC * (KV8 ? 1 : 2) == 16, uint4, uint2>::type;
+  constexpr uint32_t VB = VC * (KV8 ? 1 : 2);    // their bytes: 16, or 8
+  extern __shared__ __align__(128) uint8_t ring_mem[];
   __shared__ float sm_m[kTokenWarps][RT], sm_l[kTokenWarps][RT];
-  __shared__ __align__(16) float sm_o[kTokenWarps][RT][HD];
-  __shared__ int s_end;
+  __shared__ __align__(8) uint64_t sm_full[kTokenWarps][RING];
+  __shared__ int sm_valid[kTokenWarps][RING];
+  __shared__ float sm_scale[kTokenWarps][RING][2];
+  __shared__ int s_end, s_abort;
+  float (*sm_o)[RT][HD] = reinterpret_cast<float (*)[RT][HD]>(ring_mem);
 
   let_dependents_start();
   const int warp = warp_id(), lane = lane_id(), g = lane >> 2, t = lane & 3;
@@ -63,6 +131,11 @@ __global__ void __launch_bounds__(kTokenWarps * 32, RT == 8 && HD == 64 ? 3 : 2)
   const size_t row0 = static_cast<size_t>(bh) * p.Nq + static_cast<size_t>(gq) * p.C;
   const int len = valid_rows(p.len, b, p.Nk);
   const int32_t* list = p.blocks != nullptr ? p.blocks + (static_cast<size_t>(bh) * p.GQ + gq) * p.kb : nullptr;
+
+  if (threadIdx.x == 0) s_abort = 0;
+  if (lane < RING) mbar_init(&sm_full[warp][lane], KV8 ? 3 : 1);
+  fence_mbar_init();
+  __syncthreads();
 
   // entries of the list: up to its first negative one
   int n = list != nullptr ? p.kb : min(p.nb, (len + p.BK - 1) / p.BK);
@@ -117,38 +190,42 @@ __global__ void __launch_bounds__(kTokenWarps * 32, RT == 8 && HD == 64 ? 3 : 2)
     }
   }
 
-  constexpr int ESZ = KV8 ? 1 : 2;
-  const uint8_t* Kb = static_cast<const uint8_t*>(p.K) + static_cast<size_t>(bkv) * p.Nk * HD * ESZ;
-  const uint8_t* Vb = static_cast<const uint8_t*>(p.V) + static_cast<size_t>(bkv) * p.Nk * HD * ESZ;
-  uint4 kr[NT][LB];
-  Val vr[NT * 2][VH];
-  float ks = 1.f, vs = 1.f;
-  auto load_k = [&]() {
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int k = i * 8 + g;
-#pragma unroll
-      for (int j = 0; j < LB; ++j)
-        kr[i][j] = k < valid ? *reinterpret_cast<const uint4*>(Kb + (static_cast<size_t>(key0 + k) * HD * ESZ + j * 64 + t * 16))
-                             : make_uint4(0u, 0u, 0u, 0u);
+  // 8-bit rows are widened to fp16 (one instruction for two values; bf16 takes four), so Q is fp16 as well,
+  // and P, which is at most 1; the V scale is applied to a run's products in fp32.
+  float qs0 = 1.f, qs1 = 1.f;
+  if constexpr (KV8) {
+    qs0 = q_to_f16<LB * KS * 2>(qa);
+    if constexpr (WIDE) qs1 = q_to_f16<LB * KS * 2>(qb);
+  }
+
+  const uint8_t* Kb = static_cast<const uint8_t*>(p.K) + static_cast<size_t>(bkv) * p.Nk * L::ROW;
+  const uint8_t* Vb = static_cast<const uint8_t*>(p.V) + static_cast<size_t>(bkv) * p.Nk * L::ROW;
+  const uint32_t ring = smem_u32(ring_mem) + warp * L::WARP;
+  uint64_t* full = sm_full[warp];
+  volatile int* abort_flag = &s_abort;
+  uint32_t issued = 0;
+  // the run that advance() found into the ring's next slot, which this warp has read before
+  auto issue = [&]() {
+    const uint32_t slot = issued % RING, dst = ring + slot * 2 * L::RUN;
+    ++issued;
+    // masked keys weigh 0, but 0 times what lies in their value rows need not be 0
+    for (int k = valid; k < KC; ++k)
+      for (uint32_t e = lane * 16; e < L::ROW; e += 512)
+        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst + L::RUN + k * L::ROW + e), "r"(0u) : "memory");
+    if (KV8 && lane < 2) {
+      const float* src = (lane == 0 ? p.ks : p.vs) + static_cast<size_t>(bkv) * p.nb + blk;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&sm_scale[warp][slot][lane])), "l"(src) : "memory");
+      cp_async_arrive(full + slot);
     }
-    if (KV8) {
-      ks = p.ks[static_cast<size_t>(bkv) * p.nb + blk];
-      vs = p.vs[static_cast<size_t>(bkv) * p.nb + blk];
+    if (lane == 0) {
+      sm_valid[warp][slot] = valid;
+      const uint32_t bytes = valid * L::ROW;
+      const size_t at = static_cast<size_t>(key0) * L::ROW;
+      mbar_arrive_expect_tx(full + slot, 2 * bytes);
+      bulk_load(dst, Kb + at, bytes, full + slot);
+      bulk_load(dst + L::RUN, Vb + at, bytes, full + slot);
     }
-  };
-  // value rows 16 i + 2 t + {0, 1, 8, 9}: what the lane's P fragments of 16 keys multiply
-  auto load_v = [&]() {
-#pragma unroll
-    for (int i = 0; i < NT * 2; ++i) {
-      const int k = (i >> 2) * 16 + 2 * t + (i & 1) + (i & 2) * 4;
-#pragma unroll
-      for (int h = 0; h < VH; ++h) {
-        vr[i][h] = Val{};
-        if (k < valid)
-          vr[i][h] = *reinterpret_cast<const Val*>(Vb + (static_cast<size_t>(key0 + k) * HD + h * 64 + g * VC) * ESZ);
-      }
-    }
+    __syncwarp();
   };
 
   constexpr int OT = HD / 8;  // column tiles
@@ -160,37 +237,53 @@ __global__ void __launch_bounds__(kTokenWarps * 32, RT == 8 && HD == 64 ? 3 : 2)
     for (int i = 0; i < OT; ++i) o2[i][0] = o2[i][1] = 0.f;
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
-  bool more = advance();
-  if (more) load_k();
-  while (more) {
-    load_v();
+  bool more = true;
+#pragma unroll 1
+  for (int i = 0; i < RING - 1 && more; ++i) {
+    more = advance();
+    if (more) issue();
+  }
+#pragma unroll 1
+  for (uint32_t done = 0; done < issued; ++done) {
+    if (more) more = advance();
+    if (more) issue();  // into the slot of the run before this one
+    const uint32_t slot = done % RING;
+    if (!mbar_wait_warp(full + slot, (done / RING) & 1, abort_flag, p.wait_ns)) {
+      for (; done < issued; ++done) mbar_drain(full + done % RING, (done / RING) & 1);  // copies under way land
+      break;
+    }
+    const uint32_t kbase = ring + slot * 2 * L::RUN, vbase = kbase + L::RUN;
+    const int nvalid = sm_valid[warp][slot];
+    const float ks = KV8 ? sm_scale[warp][slot][0] : 1.f, vscale = KV8 ? sm_scale[warp][slot][1] : 1.f;
+    const float ks0 = p.scale_log2 * ks * qs0, ks1 = p.scale_log2 * ks * qs1;
     float s[NT][2], s2[WIDE ? NT : 1][2];
+    uint4 kr[NT][LB];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       s[i][0] = s[i][1] = 0.f;
       if constexpr (WIDE) s2[i][0] = s2[i][1] = 0.f;
 #pragma unroll
-      for (int j = 0; j < LB; ++j) {
-        uint32_t w[2 * KS];
-        if constexpr (KV8) {
-          e4m3_to_bf16(kr[i][j], w);
-        } else {
-          w[0] = kr[i][j].x, w[1] = kr[i][j].y, w[2] = kr[i][j].z, w[3] = kr[i][j].w;
-        }
+      for (int j = 0; j < LB; ++j) kr[i][j] = lds16(kbase + (i * 8 + g) * L::ROW + j * 64 + t * 16);
+    }
+    // key tiles innermost: their chains of products overlap
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const int q = (j * KS + k) * 2;
-          if constexpr (WIDE) mma_16816(s[i][0], s[i][1], s2[i][0], s2[i][1], qa[q], qb[q], qa[q + 1], qb[q + 1], w[2 * k], w[2 * k + 1]);
-          else mma_8816(s[i][0], s[i][1], qa[q], qa[q + 1], w[2 * k], w[2 * k + 1]);
+    for (int j = 0; j < LB; ++j) {
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const int q = (j * KS + k) * 2;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const uint32_t in[4] = {kr[i][j].x, kr[i][j].y, kr[i][j].z, kr[i][j].w};
+          uint32_t b0, b1;
+          if constexpr (KV8) e4m3x4_to_f16(in[k], b0, b1);
+          else b0 = in[2 * k], b1 = in[2 * k + 1];
+          if constexpr (WIDE) mma_16816<KV8>(s[i][0], s[i][1], s2[i][0], s2[i][1], qa[q], qb[q], qa[q + 1], qb[q + 1], b0, b1);
+          else mma_8816<KV8>(s[i][0], s[i][1], qa[q], qa[q + 1], b0, b1);
         }
       }
     }
-    const int nvalid = valid;
-    const float kscale = p.scale_log2 * ks, vscale = vs;
-    more = advance();
-    if (more) load_k();
     // softmax of the run: the row's running maximum, shared by its four lanes
-    auto soften = [&](float (*x)[2], float& m, float& l) -> float {
+    auto soften = [&](float (*x)[2], float kscale, float& m, float& l) -> float {
       float mx = -INFINITY;
 #pragma unroll
       for (int i = 0; i < NT; ++i)
@@ -216,50 +309,86 @@ __global__ void __launch_bounds__(kTokenWarps * 32, RT == 8 && HD == 64 ? 3 : 2)
       l = fmaf(l, alpha, sum);
       return alpha;
     };
-    const float al0 = soften(s, m0, l0);
+    const float al0 = soften(s, ks0, m0, l0);
     float al1 = 1.f;
-    if constexpr (WIDE) al1 = soften(s2, m1, l1);
-    if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
+    if constexpr (WIDE) al1 = soften(s2, ks1, m1, l1);
+    uint32_t pa[NT / 2][4];
+#pragma unroll
+    for (int k = 0; k < NT / 2; ++k) {
+      auto frag = [&](const float* x) { return KV8 ? pack_f16x2(x[0], x[1]) : pack_bf16x2(x[0], x[1]); };
+      pa[k][0] = frag(s[2 * k]), pa[k][2] = frag(s[2 * k + 1]);
+      pa[k][1] = pa[k][3] = 0;
+      if constexpr (WIDE) pa[k][1] = frag(s2[2 * k]), pa[k][3] = frag(s2[2 * k + 1]);
+    }
+    if (!KV8 && __any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
 #pragma unroll
       for (int i = 0; i < OT; ++i) o[i][0] *= al0, o[i][1] *= al0;
       if constexpr (WIDE)
 #pragma unroll
         for (int i = 0; i < OT; ++i) o2[i][0] *= al1, o2[i][1] *= al1;
     }
-    // O += (P * V scale) V, 16 keys at a time
+    // O += P V, 16 keys at a time; 8-bit: O = alpha O + V scale (P V)
 #pragma unroll
-    for (int k = 0; k < NT / 2; ++k) {
-      auto frag = [&](const float (*x)[2], int i) {
-        return KV8 ? pack_bf16x2(x[i][0] * vscale, x[i][1] * vscale) : pack_bf16x2(x[i][0], x[i][1]);
-      };
-      const uint32_t a0 = frag(s, 2 * k), a2 = frag(s, 2 * k + 1);
-      uint32_t a1 = 0, a3 = 0;
-      if constexpr (WIDE) a1 = frag(s2, 2 * k), a3 = frag(s2, 2 * k + 1);
+    for (int h = 0; h < VH; ++h) {
+      // value rows 16 k + 2 t + {0, 1, 8, 9}: what the lane's P fragments of 16 keys multiply
+      uint32_t vr[NT * 2][4];
 #pragma unroll
-      for (int h = 0; h < VH; ++h) {
-        const uint32_t* va = reinterpret_cast<const uint32_t*>(&vr[4 * k][h]);
-        const uint32_t* vb = reinterpret_cast<const uint32_t*>(&vr[4 * k + 1][h]);
-        const uint32_t* vc = reinterpret_cast<const uint32_t*>(&vr[4 * k + 2][h]);
-        const uint32_t* vd = reinterpret_cast<const uint32_t*>(&vr[4 * k + 3][h]);
+      for (int i = 0; i < NT * 2; ++i) {
+        const int k = (i >> 2) * 16 + 2 * t + (i & 1) + (i & 2) * 4;
+        const uint32_t a = vbase + k * L::ROW + h * 8 * VB + g * VB;
+        if constexpr (VB == 16) {
+          const uint4 u = lds16(a);
+          vr[i][0] = u.x, vr[i][1] = u.y, vr[i][2] = u.z, vr[i][3] = u.w;
+        } else {
+          asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(vr[i][0]), "=r"(vr[i][1]) : "r"(a));
+        }
+      }
+      if constexpr (KV8) {
+#pragma unroll
+        for (int j = 0; j < VC; j += 2) {
+          const int i = h * VC + j;
+          float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+          // bytes j and j + 1 of two rows side by side, then widened: tiles j and j + 1
+          constexpr uint32_t kSel[2] = {0x5140u, 0x7362u};
+          const uint32_t sel = kSel[(j & 2) >> 1];
+#pragma unroll
+          for (int k = 0; k < NT / 2; ++k) {
+            uint32_t b00, b01, b10, b11;
+            e4m3x4_to_f16(__byte_perm(vr[4 * k][j / 4], vr[4 * k + 1][j / 4], sel), b00, b10);
+            e4m3x4_to_f16(__byte_perm(vr[4 * k + 2][j / 4], vr[4 * k + 3][j / 4], sel), b01, b11);
+            if constexpr (WIDE) {
+              mma_16816<true>(c[0][0], c[0][1], c[0][2], c[0][3], pa[k][0], pa[k][1], pa[k][2], pa[k][3], b00, b01);
+              mma_16816<true>(c[1][0], c[1][1], c[1][2], c[1][3], pa[k][0], pa[k][1], pa[k][2], pa[k][3], b10, b11);
+            } else {
+              mma_8816<true>(c[0][0], c[0][1], pa[k][0], pa[k][2], b00, b01);
+              mma_8816<true>(c[1][0], c[1][1], pa[k][0], pa[k][2], b10, b11);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            o[i + e][0] = fmaf(c[e][0], vscale, o[i + e][0] * al0), o[i + e][1] = fmaf(c[e][1], vscale, o[i + e][1] * al0);
+            if constexpr (WIDE)
+              o2[i + e][0] = fmaf(c[e][2], vscale, o2[i + e][0] * al1), o2[i + e][1] = fmaf(c[e][3], vscale, o2[i + e][1] * al1);
+          }
+        }
+      } else {
 #pragma unroll
         for (int j = 0; j < VC; ++j) {
-          uint32_t b0, b1;
-          if constexpr (KV8) {  // bytes j of both rows side by side, then widened
-            const uint32_t sel = (j & 3) | ((4 + (j & 3)) << 4);
-            b0 = e4m3x2_to_bf16(__byte_perm(va[j / 4], vb[j / 4], sel));
-            b1 = e4m3x2_to_bf16(__byte_perm(vc[j / 4], vd[j / 4], sel));
-          } else {
-            const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-            b0 = __byte_perm(va[j / 2], vb[j / 2], sel);
-            b1 = __byte_perm(vc[j / 2], vd[j / 2], sel);
-          }
           const int i = h * VC + j;
-          if constexpr (WIDE) mma_16816(o[i][0], o[i][1], o2[i][0], o2[i][1], a0, a1, a2, a3, b0, b1);
-          else mma_8816(o[i][0], o[i][1], a0, a2, b0, b1);
+          const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
+#pragma unroll
+          for (int k = 0; k < NT / 2; ++k) {
+            const uint32_t b0 = __byte_perm(vr[4 * k][j / 2], vr[4 * k + 1][j / 2], sel);
+            const uint32_t b1 = __byte_perm(vr[4 * k + 2][j / 2], vr[4 * k + 3][j / 2], sel);
+            if constexpr (WIDE) mma_16816<false>(o[i][0], o[i][1], o2[i][0], o2[i][1], pa[k][0], pa[k][1], pa[k][2], pa[k][3], b0, b1);
+            else mma_8816<false>(o[i][0], o[i][1], pa[k][0], pa[k][2], b0, b1);
+          }
         }
       }
     }
+    __syncwarp();  // every lane has read the slot
   }
+  __syncthreads();  // the results lie over the rings
 
   // merge the warps: column of tile h * VC + j, place n: 64 h + n * VC + j
   auto spill = [&](const float (*x)[2], float m, float l, int row) {
