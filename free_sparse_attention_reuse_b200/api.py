@@ -351,20 +351,20 @@ E4M3 = torch.float8_e4m3fn
 BLOCK_ROWS = (32, 64, 128)      # keys of a block
 QUERY_ROWS = (1, 16, 64, 128)   # query rows that share a list
 
-# Calls that passed every check, by what the checks look at (types, shapes, strides, devices and plain
+# Calls that passed every check, by what the checks look at (types, shapes, layout, devices and plain
 # arguments; never an address): what the call needs beside its pointers.  These calls take as little as
 # ten microseconds on the device, so a repeated one does not check the same shapes again.
 _plans: dict = {}
 
 
-def _key(name, tensors, *rest):
-    """Hashable account of a call, or None for one that the checks have to look at."""
+def _lookup(*rest, tensors):
+    """(key, plan) of a call: what the checks look at, hashable, and what passed for it before.  The key is
+    None for a call that the checks have to see (an argument that is no tensor, or that cannot be a key)."""
     try:
-        k = (name, rest, tuple([None if t is None else (t.dtype, t.shape, t.stride(), t.device) for t in tensors]))
-        hash(k)
-        return k
+        k = rest + tuple([None if t is None else (t.dtype, t.shape, t.is_contiguous(), t.get_device()) for t in tensors])
+        return k, _plans.get(k)
     except (AttributeError, TypeError):
-        return None
+        return None, None
 
 
 def _keep(key, plan):
@@ -375,21 +375,38 @@ def _keep(key, plan):
     return plan
 
 
-def _here(device):
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device} but the current device is cuda:{torch.cuda.current_device()}")
+def _here(t):
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {t.device} but the current device is cuda:{torch.cuda.current_device()}")
 
 
 def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _workspace(ws, n: int, device):
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(t):
+    """The current stream's handle (without making a Stream object of it)."""
+    return _raw_stream(t.get_device()) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+# Stands in where a call writes no workspace (one CTA to each list): 256 bytes a device, never touched.
+_blanks: dict = {}
+
+
+def _workspace(ws, n: int, t):
     if ws is None:
-        return torch.empty(n, dtype=torch.uint8, device=device)
+        if n > 256:
+            return torch.empty(n, dtype=torch.uint8, device=t.device)
+        ws = _blanks.get(t.get_device())
+        if ws is None:
+            ws = _blanks[t.get_device()] = torch.empty(256, dtype=torch.uint8, device=t.device)
+        return ws
     _spec(ws, "ws", torch.uint8)
-    if ws.device != device:
-        raise ValueError(f"ws is on {ws.device}, other arguments on {device}")
+    if ws.device != t.device:
+        raise ValueError(f"ws is on {ws.device}, other arguments on {t.device}")
     return ws
 
 
@@ -518,21 +535,22 @@ def rotary(q, k, v, pos, axes, theta: float = 10000.0, pairs: str = "adjacent", 
     None, "head" (over a row, weights [d]) or "token" (over all heads of a token, weights
     [heads, d]); weights fp32 or bf16, or None for ones.  Returns Q [B, H, N, d], K and V
     [B, Hkv, N, d] contiguous (None where the input is None); out = (Q, K, V) to reuse buffers."""
-    key = _key("rotary", (q, k, v, pos, q_weight, k_weight, *(out or ())), axes if type(axes) is tuple else None, theta,
-               pairs, norm, eps) if type(axes) is tuple else None
-    plan = _plans.get(key) if key is not None else None
+    key = plan = None
+    if type(axes) is tuple:  # (q, k and v are views: their strides count)
+        key, plan = _lookup("rotary", axes, theta, pairs, norm, eps, *[t.stride() for t in (q, k, v) if isinstance(t, torch.Tensor)],
+                            tensors=(q, k, v, pos, q_weight, k_weight, *(out or ())))
     if plan is None:
         plan = _keep(key, _plan_rotary(q, k, v, pos, axes, theta, pairs, norm, q_weight, k_weight, eps, out))
     a, shapes = plan
-    dev = q.device
-    _here(dev)
+    _here(q)
     if out is None:
-        out = tuple([None if s is None else torch.empty(s, dtype=torch.bfloat16, device=dev) for s in shapes])
+        dev = q.device
+        out = [None if s is None else torch.empty(s, dtype=torch.bfloat16, device=dev) for s in shapes]
     else:
         _apart(dict(Q=out[0], K=out[1], V=out[2]), dict(q=q, k=k, v=v, pos=pos, q_weight=q_weight, k_weight=k_weight))
     Q, K, V = out
     check(_lib.load().mcs_rotary(a, _at(q), _at(k), _at(v), _at(pos), _at(q_weight), _at(k_weight), _at(Q), _at(K),
-                                 _at(V), stream_ptr()), "mcs_rotary")
+                                 _at(V), _stream(q)), "mcs_rotary")
     return Q, K, V
 
 
@@ -550,14 +568,14 @@ def _plan_means(K, BK, kv_len, means):
 def block_means(K, BK: int, kv_len=None, means=None):
     """Mean of the valid rows of every block of BK rows: fp32 [B, H, ceil(N / BK), d] (zero for a
     block without one).  kv_len: int32 [B], valid rows of each batch entry."""
-    key = _key("means", (K, kv_len, means), BK)
-    s, shape = _plans.get(key) or _keep(key, _plan_means(K, BK, kv_len, means))
-    _here(K.device)
+    key, plan = _lookup("means", BK, tensors=(K, kv_len, means))
+    s, shape = plan or _keep(key, _plan_means(K, BK, kv_len, means))
+    _here(K)
     if means is None:
         means = torch.empty(shape, dtype=torch.float32, device=K.device)
     else:
         _apart(dict(means=means), dict(K=K, kv_len=kv_len))
-    check(_lib.load().mcs_block_means(s, _at(K), BK, _at(kv_len), _at(means), stream_ptr()), "mcs_block_means")
+    check(_lib.load().mcs_block_means(s, _at(K), BK, _at(kv_len), _at(means), _stream(K)), "mcs_block_means")
     return means
 
 
@@ -588,17 +606,16 @@ def block_topk(Q, means, C: int, kb: int, BK: int, kv_len=None, blocks=None, ws=
     means: fp32 [B, Hkv, nb, d] from block_means or cache_write.  score = (mean of the query rows) .
     (mean of the block's keys), ties to the lower block.  kv_len: int32 [B], valid keys; a block
     behind them is not a candidate."""
-    key = _key("topk", (Q, means, kv_len, blocks), C, kb, BK)
-    s, shape, n = _plans.get(key) or _keep(key, _plan_topk(Q, means, C, kb, BK, kv_len, blocks))
-    dev = Q.device
-    _here(dev)
+    key, plan = _lookup("topk", C, kb, BK, tensors=(Q, means, kv_len, blocks))
+    s, shape, n = plan or _keep(key, _plan_topk(Q, means, C, kb, BK, kv_len, blocks))
+    _here(Q)
     if blocks is None:
-        blocks = torch.empty(shape, dtype=torch.int32, device=dev)
+        blocks = torch.empty(shape, dtype=torch.int32, device=Q.device)
     else:
         _apart(dict(blocks=blocks), dict(Q=Q, means=means, kv_len=kv_len))
-    ws = _workspace(ws, n, dev)
+    ws = _workspace(ws, n, Q)
     check(_lib.load().mcs_block_topk(s, _at(Q), _at(means), C, BK, kb, _at(kv_len), _at(blocks), _at(ws), ws.numel(),
-                                     stream_ptr()), "mcs_block_topk")
+                                     _stream(Q)), "mcs_block_topk")
     return blocks
 
 
@@ -652,20 +669,19 @@ def block_attn(Q, K, V, blocks, C: int, BK: int, R=None, kv_len=None, k_scale=No
     [B, Hkv, Nk / BK].  blocks: int32 [B, H, ceil(Nq / C), kb] (a list ends at its first negative
     entry), or None for every block.  kv_len: int32 [B], valid keys of each batch entry.  R: bf16
     like Q, added to the result.  A row without a key gives R (0 without R) and lse = -inf."""
-    key = _key("attn", (Q, K, V, blocks, R, kv_len, k_scale, v_scale, out, lse), C, BK, scale)
-    s, kb, n, fp8 = _plans.get(key) or _keep(key, _plan_block_attn(Q, K, V, blocks, C, BK, R, kv_len, k_scale, v_scale,
+    key, plan = _lookup("attn", C, BK, scale, tensors=(Q, K, V, blocks, R, kv_len, k_scale, v_scale, out, lse))
+    s, kb, n, fp8 = plan or _keep(key, _plan_block_attn(Q, K, V, blocks, C, BK, R, kv_len, k_scale, v_scale,
                                                                    out, lse, scale))
-    dev = Q.device
-    _here(dev)
+    _here(Q)
     if out is not None or lse is not None:
         _apart(dict(out=out, lse=lse), dict(Q=Q, K=K, V=V, R=R, blocks=blocks, kv_len=kv_len, k_scale=k_scale, v_scale=v_scale))
     if out is None:
         out = torch.empty_like(Q)
     if want_lse and lse is None:
-        lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=dev)
-    ws = _workspace(ws, n, dev)
+        lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device)
+    ws = _workspace(ws, n, Q)
     check(_lib.load().mcs_block_attn(s, _at(Q), _at(K), _at(V), fp8, _at(k_scale), _at(v_scale), _at(blocks), C, BK, kb,
-                                     _at(kv_len), _at(R), _at(out), _at(lse), _at(ws), ws.numel(), stream_ptr()),
+                                     _at(kv_len), _at(R), _at(out), _at(lse), _at(ws), ws.numel(), _stream(Q)),
           "mcs_block_attn")
     return out, lse
 
@@ -695,11 +711,11 @@ def cache_write(K, V, K8, V8, k_scale, v_scale, BK: int, start: int = 0, means=N
     given.  start and capacity are multiples of BK; a block's scale comes from this call's rows, so an
     unfinished block is lengthened by writing its rows again.  lens: int32 [B], valid rows of this
     call; rows behind them stay as they were."""
-    key = _key("write", (K, V, K8, V8, k_scale, v_scale, means, lens), BK, start)
-    s, cap = _plans.get(key) or _keep(key, _plan_write(K, V, K8, V8, k_scale, v_scale, BK, start, means, lens))
-    _here(K.device)
+    key, plan = _lookup("write", BK, start, tensors=(K, V, K8, V8, k_scale, v_scale, means, lens))
+    s, cap = plan or _keep(key, _plan_write(K, V, K8, V8, k_scale, v_scale, BK, start, means, lens))
+    _here(K)
     check(_lib.load().mcs_cache_write(s, _at(K), _at(V), BK, start, cap, _at(lens), _at(K8), _at(V8), _at(k_scale),
-                                      _at(v_scale), _at(means), stream_ptr()), "mcs_cache_write")
+                                      _at(v_scale), _at(means), _stream(K)), "mcs_cache_write")
 
 
 class KVCache:
