@@ -45,7 +45,7 @@ bool block_attn_attrs() {
   // with another count would wait for registers that never come, so it is refused here
   cudaFuncAttributes fa{};
   return cudaFuncSetAttribute(block_attn_kernel<HD, KV8, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              BlockSmem<HD>::BYTES) == cudaSuccess &&
+                              BlockSmem<HD, KV8>::BYTES) == cudaSuccess &&
          cudaFuncGetAttributes(&fa, block_attn_kernel<HD, KV8, PAIR>) == cudaSuccess &&
          static_cast<long long>(fa.numRegs) * kAttnThreads == 65536;
 }
@@ -153,7 +153,7 @@ mcs_status run_block_attn(const BlockAttnParams& p, cudaStream_t st, int sms) {
     const uint64_t rows = static_cast<uint64_t>(p.B) * p.Hkv * p.Nk;
     if (!make_row_map(&tmK, p.K, rows, HD, p.BK) || !make_row_map(&tmV, p.V, rows, HD, p.BK)) return MCS_ERR_CUDA;
   }
-  block_attn_kernel<HD, KV8, PAIR><<<std::min(p.num_units, sms), kAttnThreads, BlockSmem<HD>::BYTES, st>>>(tmQ, tmK, tmV, p);
+  block_attn_kernel<HD, KV8, PAIR><<<std::min(p.num_units, sms), kAttnThreads, BlockSmem<HD, KV8>::BYTES, st>>>(tmQ, tmK, tmV, p);
   join_parts<HD>(p, st);
   return launch_status();
 }

@@ -117,43 +117,49 @@ struct StageInfo {
   float ks[4], vs[4];
 };
 
-template <int HD>
+template <int HD, bool KV8>
 struct BlockSmem {
   static constexpr uint32_t TILE_BYTES = kTile * HD * 2;
-  static constexpr int KST = HD == 128 ? 3 : 6;
-  static constexpr int VST = HD == 128 ? 3 : 6;
+  static constexpr int KST = KV8 ? (HD == 128 ? 2 : 4) : (HD == 128 ? 3 : 6);  // K ring
+  static constexpr int VST = KST;                                            // V ring
+  static constexpr uint32_t RAW_BYTES = kTile * HD;                            // an 8-bit tile before it is widened
+  static constexpr int RAWS = KV8 ? (HD == 128 ? 4 : 8) : 0;                   // ring of those, K and V in turn
+  static constexpr int INFOS = KV8 ? 8 : KST;
   static constexpr uint32_t Q_OFF = 0;
   static constexpr uint32_t K_OFF = Q_OFF + TILE_BYTES;
   static constexpr uint32_t V_OFF = K_OFF + KST * TILE_BYTES;
-  static constexpr uint32_t XCH_OFF = V_OFF + VST * TILE_BYTES;  // 2 streams x 128 rows x (m, l)
-  static constexpr uint32_t INFO_OFF = XCH_OFF + 2 * kTile * 8;  // StageInfo[KST]
-  static constexpr uint32_t UNIT_OFF = INFO_OFF + KST * sizeof(StageInfo);  // stages of both streams, 4 units
+  static constexpr uint32_t RAW_OFF = V_OFF + VST * TILE_BYTES;
+  static constexpr uint32_t XCH_OFF = RAW_OFF + RAWS * RAW_BYTES;  // 2 streams x 128 rows x (m, l)
+  static constexpr uint32_t INFO_OFF = XCH_OFF + 2 * kTile * 8;    // StageInfo[INFOS]
+  static constexpr uint32_t UNIT_OFF = INFO_OFF + INFOS * sizeof(StageInfo);  // stages of both streams, 4 units
   static constexpr uint32_t BAR_OFF = UNIT_OFF + 4 * 8;
   // q_full, q_empty, k_full[KST], k_empty[KST], v_full[VST], v_empty[VST]; per stream s_full, p_full,
-  // pv_done, p_half, pvlo_done, s_hi; o_empty, drain, vfix[2], pair[4], u_full[4]
-  static constexpr int NBAR = 2 + 2 * KST + 2 * VST + 12 + 4 + 4 + 4;
+  // pv_done, p_half, pvlo_done, s_hi; o_empty, drain, vfix[2], pair[4], u_full[4], raw_full[RAWS], raw_empty[RAWS]
+  static constexpr int NBAR = 2 + 2 * KST + 2 * VST + 12 + 4 + 4 + 4 + 2 * RAWS;
   static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
   static constexpr uint32_t BYTES = MISC_OFF + 16;
   static_assert(BAR_OFF % 8 == 0 && INFO_OFF % 16 == 0, "shared memory alignment");
   static_assert(BYTES <= 232448, "shared memory budget");
 };
 
-// Registers a thread: softmax (two warpgroups), producers, MMA; the 8-bit form's producers hold two
-// tiles' worth of loads each.
+// Registers a thread: softmax (two warpgroups), producers, MMA (the 8-bit form's loader is one of its warps).
 template <bool KV8>
 struct BlockRegs {
-  static constexpr uint32_t SOFTMAX = KV8 ? 184 : 192, PRODUCER = KV8 ? 96 : 80, MMA = 48;
+  static constexpr uint32_t SOFTMAX = KV8 ? 184 : 192, PRODUCER = 80, MMA = KV8 ? 64 : 48;
   static_assert(2 * 128 * SOFTMAX + 128 * PRODUCER + 128 * MMA <= 512 * 128, "more registers than the launch has");
 };
 
-// 16 e4m3 values to bf16 (exact: 4 significant bits, exponents in range).
-__device__ __forceinline__ void e4m3_to_bf16(const uint4& u, uint32_t* w) {
-  const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+// 8 e4m3 values to bf16 (exact: 4 significant bits, exponents in range).
+__device__ __forceinline__ void e4m3_to_bf16(uint32_t a, uint32_t b, uint32_t* w) {
+  const uint32_t in[2] = {a, b};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __nv_fp8x2_storage_t x = static_cast<__nv_fp8x2_storage_t>(in[i >> 1] >> ((i & 1) * 16));
-    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(x, __NV_E4M3)));
-    w[i] = pack_bf16x2(f.x, f.y);
+  for (int i = 0; i < 2; ++i) {
+    uint32_t lo, hi;
+    e4m3x4_to_f16(in[i], lo, hi);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    w[2 * i] = pack_bf16x2(f.x, f.y);
+    w[2 * i + 1] = pack_bf16x2(g.x, g.y);
   }
 }
 
@@ -174,11 +180,11 @@ template <int HD, bool KV8, bool PAIR>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     block_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const BlockAttnParams p) {
-  using L = BlockSmem<HD>;
+  using L = BlockSmem<HD, KV8>;
   using RG = BlockRegs<KV8>;
   constexpr int KST = L::KST, VST = L::VST;
   constexpr uint32_t HALF = kTile * 128;
-  constexpr bool SUB = PAIR && HD == 64;               // a stream's keys in two halves, a warp pair each
+  constexpr bool SUB = PAIR && HD == 64 && !KV8;       // a stream's keys in two halves, a warp pair each
   constexpr uint32_t ACTIVE = PAIR && !SUB ? 64 : 128;  // softmax threads of a stream
   constexpr int RUNS = SUB ? 2 : 4;                     // runs of 32 keys that a softmax thread takes
   constexpr int ISSUERS = SUB ? 4 : 1;                  // MMA-issuing warps
@@ -211,6 +217,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint64_t* vfix = drain + 1;    // [2]: V stage whose last rows are cleared before it is handed on
   uint64_t* pair = vfix + 2;     // [4], one per row group (its two warps)
   uint64_t* u_full = pair + 4;   // [4], unit counts published
+  uint64_t* raw_full = u_full + 4;            // [RAWS] each: 8-bit tiles loaded, and widened
+  uint64_t* raw_empty = raw_full + L::RAWS;
   StageInfo* sInfo = reinterpret_cast<StageInfo*>(smem_raw + L::INFO_OFF);
   int2* sUnit = reinterpret_cast<int2*>(smem_raw + L::UNIT_OFF);
   float2* sXch = reinterpret_cast<float2*>(smem_raw + L::XCH_OFF);
@@ -245,7 +253,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     mbar_init(vfix, 1);
     mbar_init(vfix + 1, 1);
     for (int g = 0; g < 4; ++g) mbar_init(pair + g, 64);
-    for (int g = 0; g < 4; ++g) mbar_init(u_full + g, SUB && !KV8 ? 2 : 1);
+    for (int g = 0; g < 4; ++g) mbar_init(u_full + g, SUB ? 2 : 1);
+    for (int s = 0; s < L::RAWS; ++s) {
+      mbar_init(raw_full + s, 1);
+      mbar_init(raw_empty + s, 128);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -265,93 +277,92 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     return i < m ? 2 * i + x : m + i;
   };
 
+  const int BPS = kTile / p.BK;  // blocks of a stage
+  const int bk_log = 31 - __clz(p.BK);
+  // What a producer warp learns of a unit: the walks over its lists, at their first entries, the
+  // entries to take of each, and so the stages of both streams (`only` >= 0: of that list's alone).
+  constexpr int LISTS = PAIR ? 2 : 1;
+  struct Unit {
+    int bh, ut, bkv, len;
+    int left[LISTS], tn[2];
+  };
+  ListWalk wk[LISTS];
+  auto open_unit = [&](int unit, int only, bool report) {
+    Unit u;
+    const int sp = unit % p.splits, tu = unit / p.splits;
+    u.bh = tu / p.tiles;
+    u.ut = tu - u.bh * p.tiles;
+    const int b = u.bh / p.H;
+    u.bkv = b * p.Hkv + (u.bh - b * p.H) / (p.H / p.Hkv);
+    u.len = valid_rows(p.len, b, p.Nk);
+    u.tn[0] = u.tn[1] = 0;
+    auto open_list = [&](ListWalk& w, int x, int& left) {
+      const int g = PAIR ? 2 * u.ut + x : u.ut;
+      const bool some = g < p.GQ;  // not so: an odd last list, stream B has no rows here
+      w.list = some && p.blocks != nullptr ? p.blocks + (static_cast<size_t>(u.bh) * p.GQ + g) * p.kb : nullptr;
+      w.kb = some ? p.kb : 0;
+      w.nb = p.nb;
+      w.bk_log = bk_log;
+      w.len = u.len;
+      const int n = p.blocks != nullptr ? w.count(report) : min(p.nb, (u.len + p.BK - 1) >> bk_log);
+      const int lo = static_cast<int>(static_cast<long long>(n) * sp / p.splits);
+      left = static_cast<int>(static_cast<long long>(n) * (sp + 1) / p.splits) - lo;
+      w.start(lo);
+      return some ? max(1, (left + BPS - 1) / BPS) : 0;
+    };
+    if (only >= 0) {
+      u.tn[only] = open_list(wk[0], only, u.left[0]);
+    } else {
+#pragma unroll
+      for (int x = 0; x < LISTS; ++x) u.tn[x] = open_list(wk[x], x, u.left[x]);
+      if (!PAIR) {
+        u.tn[1] = u.tn[0] / 2;
+        u.tn[0] -= u.tn[1];
+      }
+    }
+    return u;
+  };
+  // The blocks of the next stage of walk x: their number; this lane's entries off and off2 among them
+  // (meaningless from that number on).
+  auto take = [&](Unit& u, int x, int off, int off2, int& blk, int& blk2) {
+    auto from = [&](ListWalk& w, int& left) {
+      w.ensure(BPS);
+      const int n = min(min(BPS, left), w.have - w.at);
+      blk = __shfl_sync(0xffffffffu, w.cur, (w.at + off) & 31);
+      blk2 = __shfl_sync(0xffffffffu, w.cur, (w.at + off2) & 31);
+      w.at += n;
+      left -= n;
+      return n;
+    };
+    return PAIR && x ? from(wk[LISTS - 1], u.left[LISTS - 1]) : from(wk[0], u.left[0]);
+  };
+  // The unit's counts for the other roles (`only` >= 0: that stream's), and its Q tile (after the last
+  // QK^T of the one before).  The counts' slot was last the unit's four back: the MMAs of the unit
+  // before this one are issued, so the epilogue of the one two before that has read its own.
+  auto publish = [&](const Unit& u, uint32_t u_it, int only) -> bool {
+    if (!mbar_wait_warp(q_empty, (u_it & 1) ^ 1, abort_flag, wl)) return false;
+    if (lane == 0) {
+      int2& slot = sUnit[u_it & 3];
+      if (only <= 0) slot.x = u.tn[0];
+      if (only != 0) slot.y = u.tn[1];
+      mbar_arrive(u_full + (u_it & 3));
+      if (only <= 0) {
+        mbar_arrive_expect_tx(q_full, L::TILE_BYTES);
+#pragma unroll
+        for (int h = 0; h < HD / 64; ++h)
+          tma_load_2d(sQ + h * HALF, &tmQ, h * 64, u.bh * p.Nq + u.ut * kTile, q_full);
+      }
+    }
+    __syncwarp();
+    return true;
+  };
+
   if (warp >= 8 && warp < 12) {
     // ------------------------------------------------------------------ producer
     regs_to<RG::PRODUCER, LAUNCH_REGS>();
     const int pw = warp - 8;
-    const int BPS = kTile / p.BK;  // blocks of a stage
-    const int bk_log = 31 - __clz(p.BK);
     uint32_t u_it = 0;
     bool okp = true;
-    // What a producer warp learns of a unit: the walks over its lists, at their first entries, the
-    // entries to take of each, and so the stages of both streams (`only` >= 0: of that list's alone).
-    constexpr int LISTS = PAIR ? 2 : 1;
-    struct Unit {
-      int bh, ut, bkv, len;
-      int left[LISTS], tn[2];
-    };
-    ListWalk wk[LISTS];
-    auto open_unit = [&](int unit, int only, bool report) {
-      Unit u;
-      const int sp = unit % p.splits, tu = unit / p.splits;
-      u.bh = tu / p.tiles;
-      u.ut = tu - u.bh * p.tiles;
-      const int b = u.bh / p.H;
-      u.bkv = b * p.Hkv + (u.bh - b * p.H) / (p.H / p.Hkv);
-      u.len = valid_rows(p.len, b, p.Nk);
-      u.tn[0] = u.tn[1] = 0;
-      auto open_list = [&](ListWalk& w, int x, int& left) {
-        const int g = PAIR ? 2 * u.ut + x : u.ut;
-        const bool some = g < p.GQ;  // not so: an odd last list, stream B has no rows here
-        w.list = some && p.blocks != nullptr ? p.blocks + (static_cast<size_t>(u.bh) * p.GQ + g) * p.kb : nullptr;
-        w.kb = some ? p.kb : 0;
-        w.nb = p.nb;
-        w.bk_log = bk_log;
-        w.len = u.len;
-        const int n = p.blocks != nullptr ? w.count(report) : min(p.nb, (u.len + p.BK - 1) >> bk_log);
-        const int lo = static_cast<int>(static_cast<long long>(n) * sp / p.splits);
-        left = static_cast<int>(static_cast<long long>(n) * (sp + 1) / p.splits) - lo;
-        w.start(lo);
-        return some ? max(1, (left + BPS - 1) / BPS) : 0;
-      };
-      if (only >= 0) {
-        u.tn[only] = open_list(wk[0], only, u.left[0]);
-      } else {
-#pragma unroll
-        for (int x = 0; x < LISTS; ++x) u.tn[x] = open_list(wk[x], x, u.left[x]);
-        if (!PAIR) {
-          u.tn[1] = u.tn[0] / 2;
-          u.tn[0] -= u.tn[1];
-        }
-      }
-      return u;
-    };
-    // The blocks of the next stage of walk x: their number; this lane's entries off and off2 among them
-    // (meaningless from that number on).
-    auto take = [&](Unit& u, int x, int off, int off2, int& blk, int& blk2) {
-      auto from = [&](ListWalk& w, int& left) {
-        w.ensure(BPS);
-        const int n = min(min(BPS, left), w.have - w.at);
-        blk = __shfl_sync(0xffffffffu, w.cur, (w.at + off) & 31);
-        blk2 = __shfl_sync(0xffffffffu, w.cur, (w.at + off2) & 31);
-        w.at += n;
-        left -= n;
-        return n;
-      };
-      return PAIR && x ? from(wk[LISTS - 1], u.left[LISTS - 1]) : from(wk[0], u.left[0]);
-    };
-    uint32_t q_issued = 0;
-    // The unit's counts for the other roles (`only` >= 0: that stream's), and its Q tile (after the last
-    // QK^T of the one before).  The counts' slot was last the unit's four back: the MMAs of the unit
-    // before this one are issued, so the epilogue of the one two before that has read its own.
-    auto publish = [&](const Unit& u, int only) -> bool {
-      if (!mbar_wait_warp(q_empty, (u_it & 1) ^ 1, abort_flag, wl)) return false;
-      if (lane == 0) {
-        int2& slot = sUnit[u_it & 3];
-        if (only <= 0) slot.x = u.tn[0];
-        if (only != 0) slot.y = u.tn[1];
-        mbar_arrive(u_full + (u_it & 3));
-        if (only <= 0) {
-          mbar_arrive_expect_tx(q_full, L::TILE_BYTES);
-#pragma unroll
-          for (int h = 0; h < HD / 64; ++h)
-            tma_load_2d(sQ + h * HALF, &tmQ, h * 64, u.bh * p.Nq + u.ut * kTile, q_full);
-        }
-      }
-      if (only <= 0) ++q_issued;
-      __syncwarp();
-      return true;
-    };
     if constexpr (!KV8) {
       // ---- bf16 rows by TMA, a box per block and 64 columns: warp 8 the keys, warp 9 the values; SUB:
       // of stream A's list, warps 10 and 11 those of stream B's
@@ -369,10 +380,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // lane l copies columns 64 (l % HB) .. of block l / HB of a stage, and sizes up run l % 4
         const int my_blk = lane / HB, my_col = lane % HB;
         const int run_blk = (lane & 3) * 32 >> bk_log, run_off = ((lane & 3) * 32) & (p.BK - 1);
-        uint32_t n_fix = 0, issued = 0;
+        uint32_t n_fix = 0, issued = 0, q_issued = 0;
         for (int unit = blockIdx.x; unit < p.num_units && okp; unit += gridDim.x, ++u_it) {
           Unit u = open_unit(unit, only, keys);
-          if (keys && !publish(u, only)) { okp = false; break; }
+          if (keys) {
+            if (!publish(u, u_it, only)) { okp = false; break; }
+            if (only <= 0) ++q_issued;
+          }
           const int T = u.tn[0] + u.tn[1], both = 2 * min(u.tn[0], u.tn[1]), longer = u.tn[0] >= u.tn[1] ? 0 : 1;
           for (int t = 0; t < T; ++t) {
             int blk, rb;
@@ -430,88 +444,45 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
       }
     } else {
-      // ---- 8-bit rows: every warp its run of 32 keys of each stage, widened to bf16 on the way
-      constexpr int LPR = HD / 16, RPI = 32 / LPR, NIT = 32 / RPI;
+      // ---- 8-bit tiles, loaded by warp 13, widened to bf16: every warp its run of 32 keys of each
+      constexpr int LPR = HD / 8, RPI = 32 / LPR, NIT = 32 / RPI;  // lanes to a row (8 values each), rows of a pass
       const int sub = lane / LPR, c = lane % LPR;
-      const int run_blk = pw * 32 >> bk_log, run_off = (pw * 32) & (p.BK - 1);
-      uint32_t it0 = 0, it1 = 0;  // stages so far (SUB: of stream A, of stream B)
+      constexpr uint32_t RAWS = L::RAWS;
+      uint32_t it = 0, raw = 0;  // stages, 8-bit tiles so far
+      // rows from `rows` of this warp's run on become zero
+      auto widen = [&](uint32_t src, uint32_t dst, int rows) {
+        const uint32_t from = src + (pw * 32 + sub) * HD + c * 8;
+#pragma unroll
+        for (int i = 0; i < NIT; ++i) {
+          uint32_t a, b, w[4];
+          asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "r"(from + i * RPI * HD));
+          if (i * RPI + sub >= rows) a = b = 0u;
+          e4m3_to_bf16(a, b, w);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + sw128_offset(pw * 32 + i * RPI + sub, c, kTile)),
+                       "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                       : "memory");
+        }
+        fence_proxy_async_smem();
+      };
       for (int unit = blockIdx.x; unit < p.num_units && okp; unit += gridDim.x, ++u_it) {
-        Unit u = open_unit(unit, -1, pw == 0);
-        if (pw == 0 && !publish(u, -1)) { okp = false; break; }
-        const int T = u.tn[0] + u.tn[1], both = 2 * min(u.tn[0], u.tn[1]), longer = u.tn[0] >= u.tn[1] ? 0 : 1;
-        uint4 bk[NIT], bv[NIT];
-        float fks = 1.f, fvs = 1.f;
-        int valid = 0;
-        auto fetch = [&](int t) {
-          int blk, same;
-          if (take(u, t < both ? t & 1 : longer, run_blk, run_blk, blk, same) <= run_blk) blk = -1;
-          const int row0 = blk * p.BK + run_off;
-          valid = blk < 0 ? 0 : min(32, max(0, u.len - row0));
-          fks = fvs = 1.f;
-          if (blk >= 0) {
-            fks = p.ks[static_cast<size_t>(u.bkv) * p.nb + blk];
-            fvs = p.vs[static_cast<size_t>(u.bkv) * p.nb + blk];
-          }
-          const size_t at = (static_cast<size_t>(u.bkv) * p.Nk + (blk < 0 ? 0 : row0)) * HD + c * 16;
+        if (!mbar_wait_warp(u_full + (u_it & 3), (u_it >> 2) & 1, abort_flag, wl)) break;
+        const int T = sUnit[u_it & 3].x + sUnit[u_it & 3].y;
+        for (int t = 0; t < T && okp; ++t, ++it) {
 #pragma unroll
-          for (int it = 0; it < NIT; ++it) {
-            const int r = it * RPI + sub;
-            bk[it] = r < valid ? *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.K) + at + r * HD) : make_uint4(0u, 0u, 0u, 0u);
-          }
-#pragma unroll
-          for (int it = 0; it < NIT; ++it) {
-            const int r = it * RPI + sub;
-            bv[it] = r < valid ? *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.V) + at + r * HD) : make_uint4(0u, 0u, 0u, 0u);
-          }
-        };
-        // a lane's 16 values are two 16-byte chunks; every other lane stores its second one first, so
-        // that a store's eight lanes of a row group hit all eight bank groups
-        auto put = [&](uint32_t tile, const uint4* buf) {
-#pragma unroll
-          for (int it = 0; it < NIT; ++it) {
-            uint32_t x[8];
-            e4m3_to_bf16(buf[it], x);
-            const int r = pw * 32 + it * RPI + sub;
-            const bool swap = HD == 128 ? (c & 4) != 0 : (sub & 1) != 0;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const bool second = (k == 1) != swap;
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(tile + sw128_offset(r, 2 * c + (second ? 1 : 0), kTile)),
-                           "r"(second ? x[4] : x[0]), "r"(second ? x[5] : x[1]), "r"(second ? x[6] : x[2]),
-                           "r"(second ? x[7] : x[3])
-                           : "memory");
+          for (int v = 0; v < 2; ++v, ++raw) {  // the stage's keys, then its values
+            const uint32_t rs = raw % RAWS, slot = it % KST;
+            if (!mbar_wait_warp(raw_full + rs, (raw / RAWS) & 1, abort_flag, wl) ||
+                !mbar_wait_warp((v ? v_empty : k_empty) + slot, ((it / KST) & 1) ^ 1, abort_flag, wl)) {
+              okp = false;
+              break;
             }
+            widen(base + L::RAW_OFF + rs * L::RAW_BYTES, (v ? sV : sK) + slot * L::TILE_BYTES,
+                  v ? sInfo[it % L::INFOS].valid[pw] : 32);
+            mbar_arrive((v ? v_full : k_full) + slot);
+            mbar_arrive(raw_empty + rs);
           }
-          fence_proxy_async_smem();
-        };
-        fetch(0);
-        for (int t = 0; t < T; ++t) {
-          uint32_t ks, vs, kph, vph;
-          if (SUB) {
-            const int x = t < both ? t & 1 : longer;
-            const uint32_t it = x ? it1++ : it0++;
-            ks = vs = x * (KST / 2) + it % (KST / 2);
-            kph = vph = (it / (KST / 2)) & 1;
-          } else {
-            ks = it0 % KST, kph = (it0 / KST) & 1;
-            vs = it0 % VST, vph = (it0 / VST) & 1;
-            ++it0;
-          }
-          if (!mbar_wait_warp(k_empty + ks, kph ^ 1, abort_flag, wl)) { okp = false; break; }
-          if (lane == 0) {
-            sInfo[ks].valid[pw] = valid;
-            sInfo[ks].ks[pw] = fks;
-            sInfo[ks].vs[pw] = fvs;
-          }
-          put(sK + ks * L::TILE_BYTES, bk);
-          mbar_arrive(k_full + ks);
-          if (!mbar_wait_warp(v_empty + vs, vph ^ 1, abort_flag, wl)) { okp = false; break; }
-          put(sV + vs * L::TILE_BYTES, bv);
-          mbar_arrive(v_full + vs);
-          if (t + 1 < T) fetch(t + 1);
         }
       }
-      if (!okp && pw == 0 && q_issued > 0) mbar_drain(q_full, (q_issued - 1) & 1);
     }
   } else if (warp >= 12) {
     // ------------------------------------------------------------------ MMA issuer
@@ -636,6 +607,67 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       // every MMA issued above has completed before TMEM is released
       mma_commit_warp(drain);
       mbar_drain(drain, 0);
+    } else if (KV8 && warp == 13) {
+      if constexpr (KV8) {
+        constexpr uint32_t RAWS = L::RAWS;
+        // ---- loader of the 8-bit tiles: K, then V, of every stage by bulk copies, a whole block each; its
+        // blocks' scales and valid keys for the other roles.  An entry of sInfo is written eight stages after
+        // its last use: the ring of widened tiles lets this warp no further ahead.
+        uint32_t u_it = 0, it = 0, raw = 0;
+        bool ok = true;
+        const int run_blk = (lane & 3) * 32 >> bk_log, run_off = ((lane & 3) * 32) & (p.BK - 1);
+        const uint32_t block_bytes = static_cast<uint32_t>(p.BK) * HD;
+        for (int unit = blockIdx.x; unit < p.num_units && ok; unit += gridDim.x, ++u_it) {
+          Unit u = open_unit(unit, -1, true);
+          if (!publish(u, u_it, -1)) break;
+          const int T = u.tn[0] + u.tn[1], both = 2 * min(u.tn[0], u.tn[1]), longer = u.tn[0] >= u.tn[1] ? 0 : 1;
+          // a stage ahead, so that the scales are here when the stage is: its blocks, this lane's of them,
+          // the valid keys and scales of run lane % 4
+          int n = 0, blk = 0, valid = 0;
+          float fks = 1.f, fvs = 1.f;
+          auto look = [&](int t) {
+            int rb;
+            n = take(u, t < both ? t & 1 : longer, lane, run_blk, blk, rb);
+            valid = run_blk < n ? min(32, max(0, u.len - rb * p.BK - run_off)) : 0;
+            if (run_blk < n) {
+              fks = p.ks[static_cast<size_t>(u.bkv) * p.nb + rb];
+              fvs = p.vs[static_cast<size_t>(u.bkv) * p.nb + rb];
+            }
+          };
+          look(0);
+          for (int t = 0; t < T && ok; ++t, ++it) {
+            const int cn = n, cblk = blk;
+            const size_t at = (static_cast<size_t>(u.bkv) * p.Nk + static_cast<size_t>(lane < cn ? cblk : 0) * p.BK) * HD;
+#pragma unroll
+            for (int v = 0; v < 2; ++v, ++raw) {
+              const uint32_t rs = raw % RAWS;
+              ok = mbar_wait_warp(raw_empty + rs, ((raw / RAWS) & 1) ^ 1, abort_flag, wl);
+              if (!ok) break;
+              if (v == 0 && lane < 4) {
+                StageInfo& info = sInfo[it % L::INFOS];
+                info.valid[lane] = valid;
+                info.ks[lane] = fks;
+                info.vs[lane] = fvs;
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive_expect_tx(raw_full + rs, cn * block_bytes);
+              __syncwarp();
+              if (lane < cn)
+                bulk_load(base + L::RAW_OFF + rs * L::RAW_BYTES + lane * block_bytes,
+                          static_cast<const uint8_t*>(v ? p.V : p.K) + at, block_bytes, raw_full + rs);
+              __syncwarp();
+            }
+            if (ok && t + 1 < T) look(t + 1);
+          }
+        }
+        if (*abort_flag) {  // the copies under way land before the CTA releases its shared memory
+          if (u_it > 0) mbar_drain(q_full, (u_it - 1) & 1);
+          for (uint32_t s = 0; s < RAWS && s < raw; ++s) {
+            const uint32_t last = raw - 1 - ((raw - 1 + RAWS - s) % RAWS);
+            mbar_drain(raw_full + s, (last / RAWS) & 1);
+          }
+        }
+      }
     }  // the other warps only complete the warpgroup
   } else {
     // ------------------------------------------------------------------ softmax + epilogue
@@ -670,10 +702,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           float kq[RUNS], vsq[RUNS];
 #pragma unroll
           for (int q = 0; q < RUNS; ++q) {
-            vq[q] = sInfo[slot].valid[r0 + q];
+            const StageInfo& info = sInfo[KV8 ? (kv_base + stage_pos(tn, x, i)) % L::INFOS : slot];
+            vq[q] = info.valid[r0 + q];
             all &= vq[q];
-            kq[q] = KV8 ? sl2 * sInfo[slot].ks[r0 + q] : sl2;
-            vsq[q] = KV8 ? sInfo[slot].vs[r0 + q] : 1.f;
+            kq[q] = KV8 ? sl2 * info.ks[r0 + q] : sl2;
+            vsq[q] = KV8 ? info.vs[r0 + q] : 1.f;
           }
           // the QK^T that wrote S has read its K slot: hand the slot back to the producer
           mbar_arrive(k_empty + slot);

@@ -46,11 +46,12 @@ __device__ __forceinline__ void mma_8816(float& c0, float& c1, uint32_t a0, uint
         : "+f"(c0), "+f"(c1), "=f"(x), "=f"(y)
         : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1), "f"(0.f));
 }
-// Four e4m3 values to fp16, exact: the lower two and the upper two.
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(x));
+// D = A B for fp16.
+__device__ __forceinline__ void mma_16816_zero(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -80,11 +81,6 @@ __device__ __forceinline__ float q_to_f16(uint32_t* q) {
   return __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 u;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(a));
@@ -96,8 +92,8 @@ struct TokenSmem {
   static constexpr int KC = KV8 || HD == 64 ? 32 : 16;             // keys of a run
   static constexpr uint32_t ROW = HD * (KV8 ? 1 : 2);              // bytes of a row
   static constexpr uint32_t RUN = KC * ROW;                        // of a run's keys, or values
-  static constexpr int RING = 24576 / (2 * RUN);                   // runs that a warp has in hand: 3 or 6
-  static constexpr uint32_t WARP = RING * 2 * RUN;                 // 24 KB
+  static constexpr int RING = 16384 / (2 * RUN);                   // runs that a warp has in hand: 2 or 4
+  static constexpr uint32_t WARP = RING * 2 * RUN;                 // 16 KB
   static constexpr uint32_t BYTES = kTokenWarps * WARP;            // the warps' results lie over it at the end
   static_assert(kTokenWarps * 16 * HD * 4 <= BYTES, "results fit");
 };
@@ -257,23 +253,23 @@ __global__ void __launch_bounds__(kTokenWarps * 32, 2) block_token_kernel(const 
     const float ks = KV8 ? sm_scale[warp][slot][0] : 1.f, vscale = KV8 ? sm_scale[warp][slot][1] : 1.f;
     const float ks0 = p.scale_log2 * ks * qs0, ks1 = p.scale_log2 * ks * qs1;
     float s[NT][2], s2[WIDE ? NT : 1][2];
-    uint4 kr[NT][LB];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       s[i][0] = s[i][1] = 0.f;
       if constexpr (WIDE) s2[i][0] = s2[i][1] = 0.f;
-#pragma unroll
-      for (int j = 0; j < LB; ++j) kr[i][j] = lds16(kbase + (i * 8 + g) * L::ROW + j * 64 + t * 16);
     }
     // key tiles innermost: their chains of products overlap
 #pragma unroll
     for (int j = 0; j < LB; ++j) {
+      uint4 kr[NT];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) kr[i] = lds16(kbase + (i * 8 + g) * L::ROW + j * 64 + t * 16);
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         const int q = (j * KS + k) * 2;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          const uint32_t in[4] = {kr[i][j].x, kr[i][j].y, kr[i][j].z, kr[i][j].w};
+          const uint32_t in[4] = {kr[i].x, kr[i].y, kr[i].z, kr[i].w};
           uint32_t b0, b1;
           if constexpr (KV8) e4m3x4_to_f16(in[k], b0, b1);
           else b0 = in[2 * k], b1 = in[2 * k + 1];
@@ -347,7 +343,7 @@ __global__ void __launch_bounds__(kTokenWarps * 32, 2) block_token_kernel(const 
 #pragma unroll
         for (int j = 0; j < VC; j += 2) {
           const int i = h * VC + j;
-          float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+          float c[2][4];
           // bytes j and j + 1 of two rows side by side, then widened: tiles j and j + 1
           constexpr uint32_t kSel[2] = {0x5140u, 0x7362u};
           const uint32_t sel = kSel[(j & 2) >> 1];
@@ -356,7 +352,10 @@ __global__ void __launch_bounds__(kTokenWarps * 32, 2) block_token_kernel(const 
             uint32_t b00, b01, b10, b11;
             e4m3x4_to_f16(__byte_perm(vr[4 * k][j / 4], vr[4 * k + 1][j / 4], sel), b00, b10);
             e4m3x4_to_f16(__byte_perm(vr[4 * k + 2][j / 4], vr[4 * k + 3][j / 4], sel), b01, b11);
-            if constexpr (WIDE) {
+            if (k == 0) {
+              mma_16816_zero(c[0], pa[k][0], pa[k][1], pa[k][2], pa[k][3], b00, b01);
+              mma_16816_zero(c[1], pa[k][0], pa[k][1], pa[k][2], pa[k][3], b10, b11);
+            } else if constexpr (WIDE) {
               mma_16816<true>(c[0][0], c[0][1], c[0][2], c[0][3], pa[k][0], pa[k][1], pa[k][2], pa[k][3], b00, b01);
               mma_16816<true>(c[1][0], c[1][1], c[1][2], c[1][3], pa[k][0], pa[k][1], pa[k][2], pa[k][3], b10, b11);
             } else {

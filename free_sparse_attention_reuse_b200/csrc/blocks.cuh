@@ -21,6 +21,19 @@ __device__ __forceinline__ int valid_rows(const int32_t* len, int b, int n) {
   return v;
 }
 
+// Four e4m3 values to fp16, exact: the lower two and the upper two.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
+}
+// `bytes` consecutive bytes (a multiple of 16, as both addresses are) into shared memory; completes them on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
 // ---------------------------------------------------------------------------------- means
 // means[bh, j, :] = mean of the valid rows of block j (zero where it has none).  The sum is taken in
 // fp64, which holds a sum of up to 128 bf16 values exactly unless their exponents are more than 38
