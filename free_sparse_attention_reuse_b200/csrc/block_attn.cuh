@@ -452,15 +452,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       // rows from `rows` of this warp's run on become zero
       auto widen = [&](uint32_t src, uint32_t dst, int rows) {
         const uint32_t from = src + (pw * 32 + sub) * HD + c * 8;
+#pragma unroll 1
+        for (int i0 = 0; i0 < NIT; i0 += 8) {  // eight loads under way at a time
+          uint32_t a[8], b[8];
 #pragma unroll
-        for (int i = 0; i < NIT; ++i) {
-          uint32_t a, b, w[4];
-          asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "r"(from + i * RPI * HD));
-          if (i * RPI + sub >= rows) a = b = 0u;
-          e4m3_to_bf16(a, b, w);
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + sw128_offset(pw * 32 + i * RPI + sub, c, kTile)),
-                       "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                       : "memory");
+          for (int i = 0; i < 8; ++i)
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(a[i]), "=r"(b[i]) : "r"(from + (i0 + i) * RPI * HD));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = (i0 + i) * RPI + sub;
+            uint32_t w[4];
+            if (r >= rows) a[i] = b[i] = 0u;
+            e4m3_to_bf16(a[i], b[i], w);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + sw128_offset(pw * 32 + r, c, kTile)), "r"(w[0]),
+                         "r"(w[1]), "r"(w[2]), "r"(w[3])
+                         : "memory");
+          }
         }
         fence_proxy_async_smem();
       };
@@ -468,7 +475,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (!mbar_wait_warp(u_full + (u_it & 3), (u_it >> 2) & 1, abort_flag, wl)) break;
         const int T = sUnit[u_it & 3].x + sUnit[u_it & 3].y;
         for (int t = 0; t < T && okp; ++t, ++it) {
-#pragma unroll
+#pragma unroll 1
           for (int v = 0; v < 2; ++v, ++raw) {  // the stage's keys, then its values
             const uint32_t rs = raw % RAWS, slot = it % KST;
             if (!mbar_wait_warp(raw_full + rs, (raw / RAWS) & 1, abort_flag, wl) ||
@@ -748,13 +755,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           tmem_ld_wait_regs(sr);
 #pragma unroll
           for (int q = 1; q < RUNS; ++q) reg_fence32(sr + 32 * q);
-          if (all != 32) {  // masked keys: logits of -inf, whatever was computed
+          if (__builtin_expect(all != 32, 0)) {  // masked keys: logits of -inf, whatever was computed
 #pragma unroll
             for (int c = 0; c < 32 * RUNS; ++c) sr[c] = (c & 31) < vq[c >> 5] ? sr[c] : 0xff800000u;
           }
           // Rows without a reference yet (the first stage, or every key so far masked or at -inf; O_x
           // and l are 0 then) take the stage's exact maximum.
-          if (__any_sync(0xffffffffu, m_used == -INFINITY)) {
+          if (__builtin_expect(__any_sync(0xffffffffu, m_used == -INFINITY), 0)) {
             float mx = -INFINITY;
 #pragma unroll
             for (int q = 0; q < RUNS; ++q) {
@@ -770,7 +777,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           // A stage whose P summed past 2^16 raised the reference for this one, applied once the
           // stream's previous PV has completed so that O_x and l follow.
-          if (__any_sync(0xffffffffu, m_pend > m_used)) {
+          if (__builtin_expect(__any_sync(0xffffffffu, m_pend > m_used), 0)) {
             if (!mbar_wait_warp(pv_mine, (sc - 1) & 1, abort_flag, wl)) { ok = false; break; }
             tc_fence_after();
             const float alpha = m_pend > m_used ? fast_exp2(m_used - m_pend) : 1.f;
@@ -787,7 +794,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             float2 cs;
             chunk_exps(sr + 32 * q, kq[q], vsq[q], m_used == -INFINITY ? 0.f : m_used, pk, cs);
             const bool big = !(cs.x + cs.y <= 4294967296.f);  // 2^32, or inf / NaN
-            if (__any_sync(0xffffffffu, big)) {
+            if (__builtin_expect(__any_sync(0xffffffffu, big), 0)) {
               // rare: raise this row's reference to the run's largest logit by whole octaves (so that
               // rescaling bf16 P is exact), rescale what is behind it, and redo the run
               const float mz = m_used == -INFINITY ? 0.f : m_used;
