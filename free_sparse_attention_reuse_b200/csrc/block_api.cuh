@@ -305,7 +305,7 @@ mcs_status mcs_rotary(const mcs_rotary_args* a, const void* q, const void* k, co
   p.pos_batch = a->pos_per_batch != 0;
   p.w_bf16 = a->weight_is_bf16 != 0;
   p.eps = a->eps;
-  // a token for every group of lanes of a CTA, fewer tokens (a token's heads shared among groups) where
+  // a token for every group of lanes of a CTA, fewer tokens, and a token's heads shared among groups, where
   // that leaves SMs idle
   p.T = kRotThreads / (a->d / 8);
   while (p.T > 1 && static_cast<long long>(a->B) * ((a->N + p.T - 1) / p.T) < 2ll * di->sms) p.T /= 2;
@@ -412,8 +412,17 @@ mcs_status mcs_cache_write(mcs_shape s, const void* K, const void* V, int BK, in
   p.nb = (s.N + BK - 1) / BK;
   const dim3 grid(p.nb, s.B * s.H, 2);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (s.d == 64) cache_write_kernel<64><<<grid, kCacheThreads, 0, st>>>(p);
-  else cache_write_kernel<128><<<grid, kCacheThreads, 0, st>>>(p);
+  constexpr int R64 = kCacheThreads / (64 / 16), R128 = kCacheThreads / (128 / 16);  // rows of a pass
+  if (s.d == 64) {
+    if (BK <= R64) cache_write_kernel<64, 1><<<grid, kCacheThreads, 0, st>>>(p);
+    else cache_write_kernel<64, 128 / R64><<<grid, kCacheThreads, 0, st>>>(p);
+  } else if (BK <= R128) {
+    cache_write_kernel<128, 1><<<grid, kCacheThreads, 0, st>>>(p);
+  } else if (BK <= 2 * R128) {
+    cache_write_kernel<128, 2><<<grid, kCacheThreads, 0, st>>>(p);
+  } else {
+    cache_write_kernel<128, 128 / R128><<<grid, kCacheThreads, 0, st>>>(p);
+  }
   return launch_status();
 }
 

@@ -213,8 +213,9 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const TopkPa
 }
 
 // At most kFewRows rows (one token): every mean is read once, eight lanes to a block, the rows in shared
-// memory.  Bound: reading the means (33.5 MB for 64 key heads of 1024 blocks of 128: 5 us).
-constexpr int kFewRows = 4, kFewBlocks = 32;  // rows; blocks a CTA of four warps takes
+// memory; a CTA goes through kFewBlocks blocks, the next 16 loaded while it works on these.  Bound: reading
+// the means (33.5 MB for 64 key heads of 1024 blocks of 128: 5 us).
+constexpr int kFewRows = 4, kFewBlocks = 128;
 
 template <int HD>
 __global__ void __launch_bounds__(128) block_score_few_kernel(const TopkParams p) {
@@ -223,19 +224,19 @@ __global__ void __launch_bounds__(128) block_score_few_kernel(const TopkParams p
   const int lane = lane_id(), c = lane & 7, sub = lane >> 3;
   const int kv = p.kv0 + blockIdx.z;
   const int nv = candidate_blocks(p, kv);
-  const int j0 = blockIdx.x * kFewBlocks + warp_id() * (kFewBlocks / 4);
+  const int first = blockIdx.x * kFewBlocks, last = min(nv, first + kFewBlocks);
   let_dependents_start();
   wait_for_results();  // the mean query rows
-  if (static_cast<int>(blockIdx.x) * kFewBlocks >= nv) return;
-  constexpr int IT = kFewBlocks / 16;
-  float4 v[IT][CH];
+  if (first >= nv) return;
+  const float* mk = p.means + static_cast<size_t>(kv) * p.nb * HD + c * 4;
+  float4 v[CH];
+  auto load = [&](int j) {
+    const float* row = mk + static_cast<size_t>(min(j, last - 1)) * HD;
 #pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    const int j = min(j0 + i * 4 + sub, p.nb - 1);
-#pragma unroll
-    for (int h = 0; h < CH; ++h)
-      v[i][h] = *reinterpret_cast<const float4*>(p.means + (static_cast<size_t>(kv) * p.nb + j) * HD + h * 32 + c * 4);
-  }
+    for (int h = 0; h < CH; ++h) v[h] = *reinterpret_cast<const float4*>(row + h * 32);
+  };
+  int j = first + warp_id() * 4 + sub;
+  load(j);
   for (int i = threadIdx.x; i < kFewRows * HD; i += 128) {
     const int r = i / HD, e = i - r * HD;
     const size_t at = (static_cast<size_t>(kv) * p.M + p.m0 + r) * HD + e;
@@ -244,30 +245,31 @@ __global__ void __launch_bounds__(128) block_score_few_kernel(const TopkParams p
     q[r][e] = x;
   }
   __syncthreads();
+  for (int base = first; base < last; base += 16, j += 16) {
+    double x[4 * CH];
 #pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    const int j = j0 + i * 4 + sub;
+    for (int h = 0; h < CH; ++h) x[4 * h] = v[h].x, x[4 * h + 1] = v[h].y, x[4 * h + 2] = v[h].z, x[4 * h + 3] = v[h].w;
+    load(j + 16);
     double s[kFewRows];  // side by side, so that their chains of sums overlap
 #pragma unroll
     for (int r = 0; r < kFewRows; ++r) s[r] = 0.0;
 #pragma unroll
     for (int h = 0; h < CH; ++h) {
-      const double x0 = v[i][h].x, x1 = v[i][h].y, x2 = v[i][h].z, x3 = v[i][h].w;
 #pragma unroll
       for (int r = 0; r < kFewRows; ++r) {
         const double2 y = *reinterpret_cast<const double2*>(&q[r][h * 32 + c * 4]);
         const double2 z = *reinterpret_cast<const double2*>(&q[r][h * 32 + c * 4 + 2]);
-        s[r] = fma(x0, y.x, s[r]);
-        s[r] = fma(x1, y.y, s[r]);
-        s[r] = fma(x2, z.x, s[r]);
-        s[r] = fma(x3, z.y, s[r]);
+        s[r] = fma(x[4 * h], y.x, s[r]);
+        s[r] = fma(x[4 * h + 1], y.y, s[r]);
+        s[r] = fma(x[4 * h + 2], z.x, s[r]);
+        s[r] = fma(x[4 * h + 3], z.y, s[r]);
       }
     }
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1)
 #pragma unroll
       for (int r = 0; r < kFewRows; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
-    if (c == 0 && j < nv)
+    if (c == 0 && j < last)
 #pragma unroll
       for (int r = 0; r < kFewRows; ++r)
         if (r < p.mc) p.keys[(static_cast<size_t>(blockIdx.z) * p.mc + r) * p.nb + j] = score_key(s[r]);
@@ -468,11 +470,11 @@ __device__ __forceinline__ unsigned quantise4(const float* x, float scale, float
   return lo | (hi << 16);
 }
 
-template <int HD>
+// NIT: passes of the CTA over a block (its rows / (256 / (HD / 16)), at least 1).
+template <int HD, int NIT>
 __global__ void __launch_bounds__(kCacheThreads, 4) cache_write_kernel(const CacheWriteParams p) {
   constexpr int CG = HD / 16;                       // 16-element pieces of a row
   constexpr int RG = kCacheThreads / CG;            // rows of one pass
-  constexpr int NIT = 128 / RG;                     // passes over the largest block
   constexpr int WARPS = kCacheThreads / 32;
   __shared__ unsigned wmax[WARPS];
   __shared__ double wsum[WARPS][HD];

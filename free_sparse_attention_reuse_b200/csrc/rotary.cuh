@@ -66,26 +66,36 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
                     pack_bf16x2(f[6], f[7]));
 }
 
-// 8 norm weights from element `at` on.
-__device__ __forceinline__ void load_w8(const void* w, int bf16, size_t at, float* f) {
+__device__ __forceinline__ uint2 load8(const void* p) {
+  uint2 u;
+  asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(u.x), "=r"(u.y) : "l"(p));
+  return u;
+}
+
+// 4 norm weights from element `at` on.
+__device__ __forceinline__ void load_w4(const void* w, int bf16, size_t at, float* f) {
   if (bf16) {
-    unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + at), f);
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(w) + at);
+    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+    f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
   } else {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + at);
-    const float4 a = p[0], b = p[1];
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + at);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
   }
 }
 
 // One CTA: T consecutive tokens of one batch entry.  HD / 8 lanes make a group and hold a row, 8 elements
 // each; a group keeps to one token, whose sines and cosines stay in its registers, and goes through its
-// heads (through a share of them where there are more groups than tokens), kRotRows rows in flight.
-// Bound: device memory; one row in flight and the sines in shared memory left it at 58 % of the copy rate.
+// heads (through a share of them where there are more groups than tokens), kRotRows rows in flight.  With
+// pairs in halves a lane holds four elements of the first half and their four partners (two 8-byte
+// pieces), so that nothing is exchanged; lanes beyond the halves hold eight that are not turned.
+// Bound: device memory (480p clip, head norm: 196 us, 92 % of the copy rate; one row in flight and the sines
+// in shared memory left it at 58 %; partners by shuffles left the halves form at 143 us for 403 MB).
 template <int HD, int NORM, bool HALVES>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
   constexpr int LPR = HD / 8;                 // lanes of a group
   constexpr int GROUPS = kRotThreads / LPR;   // 16 or 32
-  constexpr int PAIRS = HALVES ? 8 : 4;       // rotations that a lane's 8 elements need
   __shared__ float part[2][GROUPS];
   const int b = blockIdx.x / p.tiles, n0 = (blockIdx.x - b * p.tiles) * p.T;
   const int group = threadIdx.x / LPR, c = threadIdx.x % LPR;
@@ -93,37 +103,61 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
   const bool live = n0 + t < p.N;
   const int n = live ? n0 + t : p.N - 1;  // (idle groups follow along on the last token and store nothing)
 
-  // the partner elements of HALVES are the same 8 slots of the lane half / 8 further (or back)
-  const int hc = p.half / 8;
-  const bool lo = c < hc, hi = !lo && c < 2 * hc;
-  float2 cs[PAIRS];
+  // this lane's elements: e0 .. e0 + 3 and e1 .. e1 + 3, pairs p0 .. p0 + 3 where it turns any
+  int e0 = c * 8, e1 = e0 + 4, p0 = c * 4;
+  bool turns = p0 < p.half;
+  if (HALVES) {
+    turns = c * 4 < p.half;
+    e0 = turns ? c * 4 : 2 * p.half + (c - p.half / 4) * 8;
+    e1 = turns ? p.half + c * 4 : e0 + 4;
+  }
+  const bool whole = 2 * p.half == HD;  // every element turns
+  float2 cs[4];
 #pragma unroll
-  for (int i = 0; i < PAIRS; ++i) {
-    const int j = HALVES ? c * 8 + i - (hi ? p.half : 0) : c * 4 + i;
+  for (int i = 0; i < 4; ++i) {
     cs[i] = make_float2(1.f, 0.f);
-    if (HALVES ? lo || hi : j < p.half) {
-      const size_t at = (static_cast<size_t>(p.pos_batch ? b : 0) * p.N + n) * p.A + p.axis[j];
+    if (turns && p0 + i < p.half) {
+      const size_t at = (static_cast<size_t>(p.pos_batch ? b : 0) * p.N + n) * p.A + p.axis[p0 + i];
       const double x = p.pos_float ? static_cast<double>(static_cast<const float*>(p.pos)[at])
                                    : static_cast<double>(static_cast<const int32_t*>(p.pos)[at]);
-      const double a = x * p.turns[j];
+      const double a = x * p.turns[p0 + i];
       sincospif(2.f * static_cast<float>(a - rint(a)), &cs[i].y, &cs[i].x);
     }
   }
+  auto source = [&](int s) { return p.x[s] + b * p.sb[s] + n * p.sn[s]; };
+  auto load = [&](const __nv_bfloat16* row) {
+    if (!HALVES) return load16(row + e0);
+    const uint2 x = load8(row + e0), y = load8(row + e1);
+    return make_uint4(x.x, x.y, y.x, y.y);
+  };
+  // 8 norm weights of this lane's elements
+  auto load_w = [&](const void* w, size_t at, float* f) {
+    load_w4(w, p.w_bf16, at + e0, f);
+    load_w4(w, p.w_bf16, at + e1, f + 4);
+  };
 
   float rs[2] = {1.f, 1.f};
   if (NORM == kNormToken) {
-    // 1 / rms of the token's whole q and k
+    // 1 / rms of the token's whole q and k (the rows are read again below, from L2)
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       float ss = 0.f;
       if (p.x[s] != nullptr) {
-        const __nv_bfloat16* row = p.x[s] + b * p.sb[s] + n * p.sn[s] + c * 8;
-#pragma unroll 8
-        for (int h = share; h < p.heads[s]; h += shares) {
-          float f[8];
-          unpack8(*reinterpret_cast<const uint4*>(row + h * p.sh[s]), f);
+        const __nv_bfloat16* row = source(s);
+        for (int h0 = share; h0 < p.heads[s]; h0 += 8 * shares) {
+          uint4 u[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
+          for (int k = 0; k < 8; ++k) {
+            const int h = h0 + k * shares;
+            u[k] = h < p.heads[s] ? load16(row + h * p.sh[s] + c * 8) : make_uint4(0u, 0u, 0u, 0u);
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float f[8];
+            unpack8(u[k], f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
+          }
         }
       }
 #pragma unroll
@@ -139,64 +173,64 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
     }
   }
 
+  // A row u, normalised with 1 / rms r and weights w, and turned.
+  auto turn = [&](uint4& u, float r, const float* w) {
+    float f[8];
+    unpack8(u, f);
+    if (NORM != kNormNone) {
+      if (NORM == kNormHead) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        r = rsqrtf(ss * (1.f / HD) + p.eps);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = f[i] * r * w[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      constexpr int STEP = HALVES ? 1 : 2, PARTNER = HALVES ? 4 : 1;
+      const float x1 = f[STEP * i], x2 = f[STEP * i + PARTNER];
+      const float y1 = x1 * cs[i].x - x2 * cs[i].y, y2 = x1 * cs[i].y + x2 * cs[i].x;
+      if (whole || (turns && p0 + i < p.half)) f[STEP * i] = y1, f[STEP * i + PARTNER] = y2;
+    }
+    u = pack8(f);
+  };
+
+  const size_t step = static_cast<size_t>(p.N) * HD;  // between heads of a target
 #pragma unroll
   for (int s = 0; s < 3; ++s) {
     if (p.x[s] == nullptr) continue;
-    const __nv_bfloat16* src = p.x[s] + b * p.sb[s] + n * p.sn[s] + c * 8;
-    __nv_bfloat16* dst = p.y[s] + (static_cast<size_t>(b) * p.heads[s] * p.N + n) * HD + c * 8;
-    const size_t step = static_cast<size_t>(p.N) * HD;
+    const __nv_bfloat16* src = source(s);
+    __nv_bfloat16* dst = p.y[s] + (static_cast<size_t>(b) * p.heads[s] * p.N + n) * HD;
     float w[8];
-    if (s < 2) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = 1.f;
-      if (NORM == kNormHead && p.w[s] != nullptr) load_w8(p.w[s], p.w_bf16, c * 8, w);
-    }
+    for (int i = 0; i < 8; ++i) w[i] = 1.f;
+    const void* weights = s < 2 ? p.w[s] : nullptr;
+    if (NORM == kNormHead && weights != nullptr) load_w(weights, 0, w);
     for (int h0 = share; h0 < p.heads[s]; h0 += shares * kRotRows) {
       uint4 u[kRotRows];
 #pragma unroll
       for (int k = 0; k < kRotRows; ++k) {
         const int h = h0 + k * shares;
-        u[k] = h < p.heads[s] ? load16(src + h * p.sh[s]) : make_uint4(0u, 0u, 0u, 0u);
+        u[k] = h < p.heads[s] ? load(src + h * p.sh[s]) : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
       for (int k = 0; k < kRotRows; ++k) {
         const int h = h0 + k * shares;
-        if (s < 2) {
-          float f[8];
-          unpack8(u[k], f);
-          if (NORM != kNormNone) {
-            float r = rs[s];
-            if (NORM == kNormHead) {
-              float ss = 0.f;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
-#pragma unroll
-              for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-              r = rsqrtf(ss * (1.f / HD) + p.eps);
-            } else if (p.w[s] != nullptr) {
-              load_w8(p.w[s], p.w_bf16, static_cast<size_t>(min(h, p.heads[s] - 1)) * HD + c * 8, w);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = f[i] * r * w[i];
-          }
-          if (!HALVES) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float x1 = f[2 * i], x2 = f[2 * i + 1];
-              f[2 * i] = x1 * cs[i].x - x2 * cs[i].y;
-              f[2 * i + 1] = x1 * cs[i].y + x2 * cs[i].x;
-            }
+        if (NORM == kNormToken && weights != nullptr) load_w(weights, static_cast<size_t>(min(h, p.heads[s] - 1)) * HD, w);
+        if (s < 2) turn(u[k], rs[s < 2 ? s : 0], w);
+        if (live && h < p.heads[s]) {
+          __nv_bfloat16* out = dst + h * step;
+          if (HALVES) {
+            *reinterpret_cast<uint2*>(out + e0) = make_uint2(u[k].x, u[k].y);
+            *reinterpret_cast<uint2*>(out + e1) = make_uint2(u[k].z, u[k].w);
           } else {
-            const int from = static_cast<int>(lane_id()) + (lo ? hc : hi ? -hc : 0);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float o = __shfl_sync(0xffffffffu, f[i], from);
-              if (lo || hi) f[i] = lo ? f[i] * cs[i].x - o * cs[i].y : o * cs[i].y + f[i] * cs[i].x;
-            }
+            *reinterpret_cast<uint4*>(out + e0) = u[k];
           }
-          u[k] = pack8(f);
         }
-        if (live && h < p.heads[s]) *reinterpret_cast<uint4*>(dst + h * step) = u[k];
       }
     }
   }

@@ -81,6 +81,22 @@ def test_rotary_fused_views_and_absent_parts():
     api.sync_status()
 
 
+@pytest.mark.parametrize("norm,H,Hkv,d,N", [("head", 3, 2, 64, 50), ("token", 3, 2, 64, 50), ("token", 40, 40, 128, 21),
+                                            ("token", 70, 1, 64, 330), ("token", 16, 16, 64, 2000)])
+def test_rotary_one_weight_and_many_heads(norm, H, Hkv, d, N):
+    q, k = rnd(7, 1, N, H, d), rnd(8, 1, N, Hkv, d)
+    g = torch.Generator().manual_seed(9)
+    pos = torch.randint(0, 500, (N, 1), generator=g).int()
+    for which in (0, 1):
+        shape = [(d,), (d,)] if norm == "head" else [(H, d), (Hkv, d)]
+        w = [None, None]
+        w[which] = 1 + 0.2 * torch.randn(*shape[which], generator=g)
+        (rq, sq), (rk, sk), _ = ref.rotary(q, k, None, pos, (d // 2,), norm=norm, q_weight=w[0], k_weight=w[1])
+        Q, K, _ = api.rotary(dev(q), dev(k), None, dev(pos), (d // 2,), norm=norm, q_weight=dev(w[0]), k_weight=dev(w[1]))
+        within(Q, rq, ref.rotary_bound(rq, sq), "Q")
+        within(K, rk, ref.rotary_bound(rk, sk), "K")
+
+
 def test_rotary_zero_rows_and_large_values():
     q = rnd(6, 1, 8, 2, 64)
     q[0, 3] = 0
