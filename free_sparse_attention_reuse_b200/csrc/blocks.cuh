@@ -212,14 +212,14 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const TopkPa
   }
 }
 
-// At most kFewRows rows (one token): every mean is read once, eight lanes to a block, the rows in shared
-// memory; a CTA goes through kFewBlocks blocks, the next 16 loaded while it works on these.  Bound: reading
-// the means (33.5 MB for 64 key heads of 1024 blocks of 128: 5 us).
+// At most kFewRows rows (one token): every mean is read once, eight lanes to a block and four blocks to a
+// lane at a time, so that the rows' reads from shared memory serve four blocks (one block to a lane was
+// bound by them: 25 us).  Bound: reading the means (33.5 MB for 64 key heads of 1024 blocks of 128: 5 us).
 constexpr int kFewRows = 4, kFewBlocks = 128;
 
 template <int HD>
-__global__ void __launch_bounds__(128) block_score_few_kernel(const TopkParams p) {
-  constexpr int CH = HD / 32;  // 4-column pieces of a lane
+__global__ void __launch_bounds__(128, 4) block_score_few_kernel(const TopkParams p) {
+  constexpr int CH = HD / 32, J = 4;  // 4-column pieces of a lane; blocks of a lane
   __shared__ __align__(16) double q[kFewRows][HD];
   const int lane = lane_id(), c = lane & 7, sub = lane >> 3;
   const int kv = p.kv0 + blockIdx.z;
@@ -229,14 +229,6 @@ __global__ void __launch_bounds__(128) block_score_few_kernel(const TopkParams p
   wait_for_results();  // the mean query rows
   if (first >= nv) return;
   const float* mk = p.means + static_cast<size_t>(kv) * p.nb * HD + c * 4;
-  float4 v[CH];
-  auto load = [&](int j) {
-    const float* row = mk + static_cast<size_t>(min(j, last - 1)) * HD;
-#pragma unroll
-    for (int h = 0; h < CH; ++h) v[h] = *reinterpret_cast<const float4*>(row + h * 32);
-  };
-  int j = first + warp_id() * 4 + sub;
-  load(j);
   for (int i = threadIdx.x; i < kFewRows * HD; i += 128) {
     const int r = i / HD, e = i - r * HD;
     const size_t at = (static_cast<size_t>(kv) * p.M + p.m0 + r) * HD + e;
@@ -245,34 +237,46 @@ __global__ void __launch_bounds__(128) block_score_few_kernel(const TopkParams p
     q[r][e] = x;
   }
   __syncthreads();
-  for (int base = first; base < last; base += 16, j += 16) {
-    double x[4 * CH];
+  for (int j0 = first + warp_id() * 4 + sub; j0 - sub < last; j0 += 16 * J) {
+    float4 v[J][CH];
 #pragma unroll
-    for (int h = 0; h < CH; ++h) x[4 * h] = v[h].x, x[4 * h + 1] = v[h].y, x[4 * h + 2] = v[h].z, x[4 * h + 3] = v[h].w;
-    load(j + 16);
-    double s[kFewRows];  // side by side, so that their chains of sums overlap
+    for (int k = 0; k < J; ++k)
 #pragma unroll
-    for (int r = 0; r < kFewRows; ++r) s[r] = 0.0;
+      for (int h = 0; h < CH; ++h)
+        v[k][h] = *reinterpret_cast<const float4*>(mk + static_cast<size_t>(min(j0 + k * 16, last - 1)) * HD + h * 32);
+    double s[J][kFewRows];
+#pragma unroll
+    for (int k = 0; k < J; ++k)
+#pragma unroll
+      for (int r = 0; r < kFewRows; ++r) s[k][r] = 0.0;
 #pragma unroll
     for (int h = 0; h < CH; ++h) {
 #pragma unroll
-      for (int r = 0; r < kFewRows; ++r) {
-        const double2 y = *reinterpret_cast<const double2*>(&q[r][h * 32 + c * 4]);
-        const double2 z = *reinterpret_cast<const double2*>(&q[r][h * 32 + c * 4 + 2]);
-        s[r] = fma(x[4 * h], y.x, s[r]);
-        s[r] = fma(x[4 * h + 1], y.y, s[r]);
-        s[r] = fma(x[4 * h + 2], z.x, s[r]);
-        s[r] = fma(x[4 * h + 3], z.y, s[r]);
+      for (int e = 0; e < 4; e += 2) {
+        double2 y[kFewRows];
+#pragma unroll
+        for (int r = 0; r < kFewRows; ++r) y[r] = *reinterpret_cast<const double2*>(&q[r][h * 32 + c * 4 + e]);
+#pragma unroll
+        for (int k = 0; k < J; ++k) {
+          const double x0 = e == 0 ? v[k][h].x : v[k][h].z, x1 = e == 0 ? v[k][h].y : v[k][h].w;
+#pragma unroll
+          for (int r = 0; r < kFewRows; ++r) s[k][r] = fma(x1, y[r].y, fma(x0, y[r].x, s[k][r]));
+        }
       }
     }
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1)
+    for (int r = 0; r < kFewRows; ++r) {
+      if (r >= p.mc) break;
 #pragma unroll
-      for (int r = 0; r < kFewRows; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
-    if (c == 0 && j < last)
+      for (int o = 4; o > 0; o >>= 1)
 #pragma unroll
-      for (int r = 0; r < kFewRows; ++r)
-        if (r < p.mc) p.keys[(static_cast<size_t>(blockIdx.z) * p.mc + r) * p.nb + j] = score_key(s[r]);
+        for (int k = 0; k < J; ++k) s[k][r] += __shfl_xor_sync(0xffffffffu, s[k][r], o);
+#pragma unroll
+      for (int k = 0; k < J; ++k) {
+        const int j = j0 + k * 16;
+        if (c == 0 && j < last) p.keys[(static_cast<size_t>(blockIdx.z) * p.mc + r) * p.nb + j] = score_key(s[k][r]);
+      }
+    }
   }
 }
 
