@@ -137,7 +137,8 @@ struct BlockSmem {
   // pv_done, p_half, pvlo_done, s_hi; o_empty, drain, vfix[2], pair[4], u_full[4], raw_full[RAWS], raw_empty[RAWS]
   static constexpr int NBAR = 2 + 2 * KST + 2 * VST + 12 + 4 + 4 + 4 + 2 * RAWS;
   static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
-  static constexpr uint32_t BYTES = MISC_OFF + 16;
+  static constexpr uint32_t QEXP_OFF = MISC_OFF + 16;  // 8-bit form: exponents of Q's rows, two units
+  static constexpr uint32_t BYTES = QEXP_OFF + (KV8 ? 2 * kTile : 0);
   static_assert(BAR_OFF % 8 == 0 && INFO_OFF % 16 == 0, "shared memory alignment");
   static_assert(BYTES <= 232448, "shared memory budget");
 };
@@ -189,7 +190,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   constexpr int RUNS = SUB ? 2 : 4;                     // runs of 32 keys that a softmax thread takes
   constexpr int ISSUERS = SUB ? 4 : 1;                  // MMA-issuing warps
   static_assert(!SUB || (KST == VST && KST % 2 == 0), "SUB: each stream has half the slots");
-  constexpr uint32_t IDESC_QK = idesc_bf16(128, 32 * RUNS, false, false);
+  // (8-bit form: Q and K in fp16, whose two format fields are 0)
+  constexpr uint32_t IDESC_QK = idesc_bf16(128, 32 * RUNS, false, false) & ~(KV8 ? (1u << 7 | 1u << 10) : 0u);
   constexpr uint32_t IDESC_PV = idesc_bf16(128, HD, false, true);
   constexpr uint32_t LAUNCH_REGS = 65536 / kAttnThreads;
 
@@ -217,6 +219,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint64_t* vfix = drain + 1;    // [2]: V stage whose last rows are cleared before it is handed on
   uint64_t* pair = vfix + 2;     // [4], one per row group (its two warps)
   uint64_t* u_full = pair + 4;   // [4], unit counts published
+  uint64_t* q_ready = KV8 ? vfix : q_full;   // Q as the MMAs read it (8-bit form: once it is fp16)
+  uint8_t* sQexp = smem_raw + L::QEXP_OFF;
   uint64_t* raw_full = u_full + 4;            // [RAWS] each: 8-bit tiles loaded, and widened
   uint64_t* raw_empty = raw_full + L::RAWS;
   StageInfo* sInfo = reinterpret_cast<StageInfo*>(smem_raw + L::INFO_OFF);
@@ -250,7 +254,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     mbar_init(o_empty, 2 * ACTIVE);
     mbar_init(drain, ISSUERS);
-    mbar_init(vfix, 1);
+    mbar_init(vfix, KV8 ? 128 : 1);
     mbar_init(vfix + 1, 1);
     for (int g = 0; g < 4; ++g) mbar_init(pair + g, 64);
     for (int g = 0; g < 4; ++g) mbar_init(u_full + g, SUB ? 2 : 1);
@@ -449,24 +453,47 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int sub = lane / LPR, c = lane % LPR;
       constexpr uint32_t RAWS = L::RAWS;
       uint32_t it = 0, raw = 0;  // stages, 8-bit tiles so far
+      // keys to fp16 (one instruction for two values), values to bf16 (P times their scale has its range; four);
       // rows from `rows` of this warp's run on become zero
-      auto widen = [&](uint32_t src, uint32_t dst, int rows) {
+      auto widen = [&](uint32_t src, uint32_t dst, int rows, bool keys) {
         const uint32_t from = src + (pw * 32 + sub) * HD + c * 8;
+        // (a loop for each, rolled: with both in one, or eight loads unrolled, their code drove the softmax's out
+        // of the instruction cache, 505 and 615 us against 484)
+        if (keys) {
 #pragma unroll 1
-        for (int i0 = 0; i0 < NIT; i0 += 8) {  // eight loads under way at a time
-          uint32_t a[8], b[8];
+          for (int i0 = 0; i0 < NIT; i0 += 4) {  // four loads under way at a time
+            uint32_t a[4], b[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(a[i]), "=r"(b[i]) : "r"(from + (i0 + i) * RPI * HD));
+            for (int i = 0; i < 4; ++i)
+              asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(a[i]), "=r"(b[i]) : "r"(from + (i0 + i) * RPI * HD));
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = (i0 + i) * RPI + sub;
-            uint32_t w[4];
-            if (r >= rows) a[i] = b[i] = 0u;
-            e4m3_to_bf16(a[i], b[i], w);
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + sw128_offset(pw * 32 + r, c, kTile)), "r"(w[0]),
-                         "r"(w[1]), "r"(w[2]), "r"(w[3])
-                         : "memory");
+            for (int i = 0; i < 4; ++i) {
+              const int r = (i0 + i) * RPI + sub;
+              uint32_t w[4];
+              e4m3x4_to_f16(a[i], w[0], w[1]);
+              e4m3x4_to_f16(b[i], w[2], w[3]);
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + sw128_offset(pw * 32 + r, c, kTile)), "r"(w[0]),
+                           "r"(w[1]), "r"(w[2]), "r"(w[3])
+                           : "memory");
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int i0 = 0; i0 < NIT; i0 += 4) {  // four loads under way at a time
+            uint32_t a[4], b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(a[i]), "=r"(b[i]) : "r"(from + (i0 + i) * RPI * HD));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = (i0 + i) * RPI + sub;
+              uint32_t w[4];
+              if (r >= rows) a[i] = b[i] = 0u;
+              e4m3_to_bf16(a[i], b[i], w);
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + sw128_offset(pw * 32 + r, c, kTile)), "r"(w[0]),
+                           "r"(w[1]), "r"(w[2]), "r"(w[3])
+                           : "memory");
+            }
           }
         }
         fence_proxy_async_smem();
@@ -474,6 +501,32 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       for (int unit = blockIdx.x; unit < p.num_units && okp; unit += gridDim.x, ++u_it) {
         if (!mbar_wait_warp(u_full + (u_it & 3), (u_it >> 2) & 1, abort_flag, wl)) break;
         const int T = sUnit[u_it & 3].x + sUnit[u_it & 3].y;
+        // Q to fp16 in place, a row a thread: times the power of two that brings its largest element into
+        // [2^14, 2^15), whose exponent the softmax gets (exact down to 2^-28 of that element, off by at
+        // most 2^-40 of it below)
+        if (!mbar_wait_warp(q_full, u_it & 1, abort_flag, wl)) break;
+        const int row = pw * 32 + lane;
+        uint32_t top = 0;
+#pragma unroll 4
+        for (int k = 0; k < HD / 8; ++k) {
+          const uint4 x = lds16(sQ + sw128_offset(row, k, kTile));
+          top = __vmaxu2(__vmaxu2(top, x.x & 0x7fff7fffu), __vmaxu2(x.y & 0x7fff7fffu, __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+        }
+        const int e = min(max(static_cast<int>(max(top & 0xffffu, top >> 16) >> 7), 20), 254) - 127;
+        const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+#pragma unroll 2
+        for (int k = 0; k < HD / 8; ++k) {
+          const uint32_t a = sQ + sw128_offset(row, k, kTile);
+          float f[8];
+          unpack8(lds16(a), f);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(pack_f16x2(f[0] * up, f[1] * up)),
+                       "r"(pack_f16x2(f[2] * up, f[3] * up)), "r"(pack_f16x2(f[4] * up, f[5] * up)),
+                       "r"(pack_f16x2(f[6] * up, f[7] * up))
+                       : "memory");
+        }
+        sQexp[(u_it & 1) * kTile + row] = static_cast<uint8_t>(e + 128);
+        fence_proxy_async_smem();
+        mbar_arrive(q_ready);
         for (int t = 0; t < T && okp; ++t, ++it) {
 #pragma unroll 1
           for (int v = 0; v < 2; ++v, ++raw) {  // the stage's keys, then its values
@@ -484,7 +537,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               break;
             }
             widen(base + L::RAW_OFF + rs * L::RAW_BYTES, (v ? sV : sK) + slot * L::TILE_BYTES,
-                  v ? sInfo[it % L::INFOS].valid[pw] : 32);
+                  v ? sInfo[it % L::INFOS].valid[pw] : 32, v == 0);
             mbar_arrive((v ? v_full : k_full) + slot);
             mbar_arrive(raw_empty + rs);
           }
@@ -576,7 +629,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (!ok) break;
           const int2 tn = sUnit[u_it & 3];
           const int T = tn.x + tn.y, both = 2 * min(tn.x, tn.y), longer = tn.x >= tn.y ? 0 : 1;
-          ok = mbar_wait_warp(q_full, u_it & 1, abort_flag, wl) && wait_at(k_full, kv_base, KST) &&
+          ok = mbar_wait_warp(q_ready, u_it & 1, abort_flag, wl) && wait_at(k_full, kv_base, KST) &&
                (both == 0 || wait_at(k_full, kv_base + 1, KST));
           if (!ok) break;
           qk_mmas(kv_base % KST, 0, 0);
@@ -700,10 +753,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (!mbar_wait_warp(u_full + (u_it & 3), (u_it >> 2) & 1, abort_flag, wl)) { ok = false; break; }
         const int2 tn = sUnit[u_it & 3];
         const int Tx = x ? tn.y : tn.x;
+        float qscale = sl2;
         float m_used = -INFINITY, l_part = 0.f;  // -inf: no key of weight yet
         float m_pend = -INFINITY;  // a raise of the reference decided by the stream's previous stage
         for (int i = 0; i < Tx; ++i, ++sc) {
           if (!mbar_wait_warp(s_mine, sc & 1, abort_flag, wl)) { ok = false; break; }
+          if (KV8 && i == 0)  // the power of two that Q's row was brought up by, taken back
+            qscale = sl2 * __uint_as_float(static_cast<uint32_t>(sQexp[(u_it & 1) * kTile + row] - 128 - 14 + 127) << 23);
           const uint32_t slot = SUB ? x * (KST / 2) + sc % (KST / 2) : (kv_base + stage_pos(tn, x, i)) % KST;
           int vq[RUNS], all = 32;
           float kq[RUNS], vsq[RUNS];
@@ -712,7 +768,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const StageInfo& info = sInfo[KV8 ? (kv_base + stage_pos(tn, x, i)) % L::INFOS : slot];
             vq[q] = info.valid[r0 + q];
             all &= vq[q];
-            kq[q] = KV8 ? sl2 * info.ks[r0 + q] : sl2;
+            kq[q] = KV8 ? qscale * info.ks[r0 + q] : sl2;
             vsq[q] = KV8 ? info.vs[r0 + q] : 1.f;
           }
           // the QK^T that wrote S has read its K slot: hand the slot back to the producer

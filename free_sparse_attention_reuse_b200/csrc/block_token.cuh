@@ -53,10 +53,6 @@ __device__ __forceinline__ void mma_16816_zero(float* d, uint32_t a0, uint32_t a
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 // A row of Q as fp16 fragments: times the power of two that brings its largest element into [2^14, 2^15),
 // which `unscale` takes back.  Exact for elements down to 2^-28 of the largest, off by at most 2^-40 of
 // it below.  (A row with infinities or NaN gives NaN either way.)
@@ -79,12 +75,6 @@ __device__ __forceinline__ float q_to_f16(uint32_t* q) {
     q[i] = pack_f16x2(f.x * up, f.y * up);
   }
   return __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
-}
-
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 u;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(a));
-  return u;
 }
 
 template <int HD, bool KV8>
