@@ -493,3 +493,139 @@ def test_block_attn_captured_replayed_and_on_other_streams(C, Nq, fp8):
         torch.cuda.synchronize()
         assert torch.equal(o, want) and torch.equal(l, wl) and torch.equal(m, m2) and torch.equal(t, t2)
     api.sync_status()
+
+
+# ------------------------------------------------------------------------------------------ the far ends
+def test_block_topk_in_parts():
+    """More rows than one part's score keys hold: rows of one key head, and key heads, in turn."""
+    for B, Hkv, rep, Nq in ((1, 1, 1, 40000), (3, 1, 2, 9000)):
+        q, k = dev(rnd(100, B, Hkv * rep, Nq, 64)), dev(rnd(101, B, Hkv, 32000, 64))
+        mk = api.block_means(k, 32)
+        got = api.block_topk(q, mk, 1, 5, 32)
+        for lo in range(0, Nq, 3000):
+            part = q[:, :, lo:lo + 3000].contiguous()
+            assert torch.equal(got[:, :, lo:lo + 3000], api.block_topk(part, mk, 1, 5, 32))
+    api.sync_status()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("C,Nq,BK", [(128, 128, 128), (64, 100, 32), (16, 16, 64), (1, 2, 64)])
+def test_block_attn_offsets_past_32_bits(C, Nq, BK, fp8):
+    """Blocks at the end of a store of 2^24 rows (4 GB of keys in bf16) give what they give in a short one."""
+    Nk, d, n = 1 << 24, 128, 512
+    dt = E4M3 if fp8 else torch.bfloat16
+    q, k, v = dev(rnd(110, 1, 1, Nq, d)), rnd(111, 1, 1, n, d), rnd(112, 1, 1, n, d)
+    kw, kw_far = {}, {}
+    if fp8:
+        (k, ks), (v, vs) = quantised(k, BK), quantised(v, BK)
+        kw = dict(k_scale=dev(ks), v_scale=dev(vs))
+        kw_far = {x: torch.ones(1, 1, Nk // BK, device=DEV) for x in kw}
+        for x in kw:
+            kw_far[x][..., -(n // BK):] = kw[x]
+    far = [torch.empty(1, 1, Nk, d, dtype=torch.uint8 if fp8 else dt, device=DEV) for _ in range(2)]
+    for t, x in zip(far, (k, v)):
+        t[:, :, -n:] = dev(x.view(torch.uint8) if fp8 else x)
+    far = [t.view(dt) for t in far]
+    gq, nb = -(-Nq // C), n // BK
+    ids = torch.randperm(nb, generator=torch.Generator().manual_seed(113))[:max(1, nb - 1)].int()
+    ids = dev(ids.expand(1, 1, gq, -1).contiguous())
+    want, wl = api.block_attn(q, dev(k), dev(v), ids, C, BK, want_lse=True, **kw)
+    got, gl = api.block_attn(q, *far, ids + (Nk - n) // BK, C, BK, want_lse=True, **kw_far)
+    api.sync_status()
+    assert torch.equal(got, want) and torch.equal(gl, wl)
+
+
+def test_cache_write_past_32_bits():
+    cap, d, BK, n = 1 << 24, 128, 64, 200
+    start = cap - 256
+    k, v = dev(rnd(120, 1, 2, n, d)), dev(rnd(121, 1, 2, n, d))
+    far = [torch.empty(1, 2, cap, d, dtype=torch.uint8, device=DEV).view(E4M3) for _ in range(2)]
+    near = [torch.empty(1, 2, 256, d, dtype=torch.uint8, device=DEV).view(E4M3) for _ in range(2)]
+    sc = [torch.empty(1, 2, m // BK, device=DEV) for m in (cap, cap, 256, 256)]
+    mk = [torch.empty(1, 2, m // BK, d, device=DEV) for m in (cap, 256)]
+    api.cache_write(k, v, *far, sc[0], sc[1], BK, start=start, means=mk[0])
+    api.cache_write(k, v, *near, sc[2], sc[3], BK, means=mk[1])
+    for a, b in zip(far, near):
+        assert torch.equal(a.view(torch.uint8)[:, :, start:start + n], b.view(torch.uint8)[:, :, :n])
+    assert torch.equal(sc[0][..., -4:], sc[2]) and torch.equal(sc[1][..., -4:], sc[3]) and torch.equal(mk[0][:, :, -4:], mk[1])
+    api.sync_status()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("C,Nq,kb", [(128, 700, 9), (64, 700, 9), (64, 100, 200)])
+def test_block_attn_wait_that_runs_out(C, Nq, kb, d, fp8):
+    """A flag that nothing sets, within 20 ms: every role gives up, the call is reported, the next is right."""
+    Nk, BK = 16384, 64
+    q, k, v = dev(rnd(130, 1, 2, Nq, d)), rnd(131, 1, 2, Nk, d), rnd(132, 1, 2, Nk, d)
+    kw = {}
+    if fp8:
+        (k, ks), (v, vs) = quantised(k, BK), quantised(v, BK)
+        kw = dict(k_scale=dev(ks), v_scale=dev(vs))
+    k, v = dev(k), dev(v)
+    ids = dev(lists(133, 1, 2, -(-Nq // C), Nk // BK, kb, "holes"))
+    want = api.block_attn(q, k, v, ids, C, BK, want_lse=True, **kw)
+    api.sync_status()
+    flag = torch.zeros(1, dtype=torch.int32, device=DEV)
+    lib = _lib.load()
+    lib.mcs_set_attn_wait_limit(20_000_000, _lib.ptr(flag))
+    try:
+        api.block_attn(q, k, v, ids, C, BK, want_lse=True, **kw)
+        with pytest.raises(_lib.MCSError) as e:
+            api.sync_status()
+        assert e.value.status == 7
+    finally:
+        lib.mcs_set_attn_wait_limit(0, None)
+    got = api.block_attn(q, k, v, ids, C, BK, want_lse=True, **kw)
+    api.sync_status()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    flag.fill_(1)
+    lib.mcs_set_attn_wait_limit(20_000_000, _lib.ptr(flag))
+    try:
+        got = api.block_attn(q, k, v, ids, C, BK, want_lse=True, **kw)
+        api.sync_status()
+    finally:
+        lib.mcs_set_attn_wait_limit(0, None)
+    assert torch.equal(got[0], want[0])
+
+
+def test_cache_refuses_a_captured_append_and_keeps_its_place():
+    cache = api.KVCache(1, 1, 64, 64, BK=32)
+    k = dev(rnd(140, 1, 1, 8, 64))
+    cache.append(k, k)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError, match="captured"):
+            cache.append(k, k)
+        out, _ = cache.attend(k[:, :, :1].contiguous(), C=1)
+    assert cache.length == 8
+    graph.replay()
+    want, _ = cache.attend(k[:, :, :1].contiguous(), C=1)
+    assert torch.equal(out, want)
+
+
+def test_empty_cache_gives_the_residual():
+    cache = api.KVCache(2, 2, 64, 64, BK=32)
+    q, r = dev(rnd(141, 2, 4, 5, 64)), dev(rnd(142, 2, 4, 5, 64))
+    for kw in (dict(C=1), dict(C=1, kb=2), dict(C=64), dict(C=64, kb=1), dict(C=128)):
+        out, lse = cache.attend(q, R=r, want_lse=True, **kw)
+        assert torch.equal(out, r) and bool((lse == -math.inf).all())
+    api.sync_status()
+
+
+def test_given_outputs_and_workspace():
+    q, k = dev(rnd(143, 1, 2, 3, 64)), dev(rnd(144, 1, 2, 5000, 64))
+    want, wl = api.block_attn(q, k, k, None, 1, 32, want_lse=True)
+    out, lse = torch.empty_like(q), torch.empty(1, 2, 3, device=DEV)
+    n = _lib.load().mcs_block_attn_workspace_size(_lib.BlockShape(1, 2, 2, 3, 5000, 64, 0.0), 1, 32, -(-5000 // 32))
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    o, l = api.block_attn(q, k, k, None, 1, 32, out=out, lse=lse, ws=ws)
+    assert o is out and l is lse and torch.equal(out, want) and torch.equal(lse, wl)
+    with pytest.raises(_lib.MCSError):
+        api.block_attn(q, k, k, None, 1, 32, ws=ws[:256])
+    with pytest.raises(ValueError, match="share"):
+        api.block_attn(q, k, k, None, 1, 32, out=q)
+    mk = api.block_means(k, 32)
+    with pytest.raises(ValueError, match="share"):
+        api.block_topk(q, mk, 1, 2, 32, blocks=mk.view(torch.int32).flatten()[:12].view(1, 2, 3, 2))
+    api.sync_status()
