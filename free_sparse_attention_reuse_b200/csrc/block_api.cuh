@@ -290,13 +290,29 @@ mcs_status mcs_rotary(const mcs_rotary_args* a, const void* q, const void* k, co
   p.w[0] = q_weight;
   p.w[1] = k_weight;
   p.pos = pos;
-  constexpr double kTwoPi = 6.283185307179586476925;
-  int at = 0;
-  for (int i = 0; i < a->axes; ++i)
-    for (int j = 0; j < a->axis_dim[i] / 2; ++j, ++at) {
-      p.turns[at] = std::pow(a->theta, -2.0 * j / a->axis_dim[i]) / kTwoPi;
-      p.axis[at] = static_cast<unsigned char>(i);
-    }
+  // the frequencies of a model's layers are the same call after call: the last table of this thread is kept
+  // (64 powers take longer than the rest of a small call's host work)
+  struct Table {
+    double theta = 0, turns[64];
+    int axes = 0, dim[kRotMaxAxes], half = 0;
+    unsigned char axis[64];
+  };
+  static thread_local Table tab;
+  if (tab.axes != a->axes || tab.theta != a->theta || std::memcmp(tab.dim, a->axis_dim, sizeof(int) * a->axes) != 0) {
+    constexpr double kTwoPi = 6.283185307179586476925;
+    tab.half = 0;
+    for (int i = 0; i < a->axes; ++i)
+      for (int j = 0; j < a->axis_dim[i] / 2; ++j, ++tab.half) {
+        tab.turns[tab.half] = std::pow(a->theta, -2.0 * j / a->axis_dim[i]) / kTwoPi;
+        tab.axis[tab.half] = static_cast<unsigned char>(i);
+      }
+    tab.theta = a->theta;
+    tab.axes = a->axes;
+    std::memcpy(tab.dim, a->axis_dim, sizeof(int) * a->axes);
+  }
+  const int at = tab.half;
+  std::memcpy(p.turns, tab.turns, sizeof(double) * at);
+  std::memcpy(p.axis, tab.axis, at);
   p.B = a->B;
   p.N = a->N;
   p.A = a->axes;

@@ -184,7 +184,8 @@ mcs_status mcs_perquery_attn(mcs_shape s, const void* Q, const void* K, const vo
                              size_t ws_bytes, void* stream);
 
 /* Failure-path hook of the attention kernels (those of mcs_dense_attn, mcs_sparse_attn,
- * mcs_residual, mcs_sparse_attn_host and the dense and residual launches of mcs_anchor), for
+ * mcs_residual, mcs_sparse_attn_host, the dense and residual launches of mcs_anchor, and
+ * mcs_block_attn, whose form for few rows has no tensor-core issuer and takes ns alone), for
  * tests and diagnosis; the pages have no counterpart.  For every such kernel enqueued after
  * this call, process-wide:
  *   - ns bounds any single wait inside the kernel, in nanoseconds (0 restores the default of
