@@ -86,12 +86,19 @@ struct BlockPlan {
 constexpr int kPlanSms = 148;
 constexpr long long kTokenCtas = 888;
 
-BlockPlan plan_block_attn(const mcs_block_shape& s, int C, int BK, int kb, bool listed) {
+BlockPlan plan_block_attn(const mcs_block_shape& s, int C, int BK, int kb, bool listed, bool kv8) {
   BlockPlan q{};
   q.H = listed ? s.H : s.Hkv;
   q.Nq = listed ? s.Nq : s.Nq * (s.H / s.Hkv);
   q.C = C;
-  q.tensor = listed ? C >= 64 : q.Nq > 16;
+  // Lists of 64 and 128 rows fill a tile; those of 1 and 16 do not.  Without lists the few-row kernel reads
+  // the store once for every 16 rows and the tiles once for every 128, but the latter start and end
+  // slower.  us, few rows | tiles, for B Hkv Nk key rows of 128 (64 for 30 k): bf16, 256 k keys, 8 rows 31 | 28,
+  // 16 rows 42 | 29, 64 rows 107 | 30; 30 k keys, 16 rows 14 | 20, 64 rows 21 | 21, 128 rows 25 | 22; 2 k keys,
+  // 128 rows 11 | 16.  8 bits: 960 k keys, 16 rows 77 | 103, 24 rows 123 | 104; 256 k keys, 16 rows 39 | 37,
+  // 24 rows 51 | 37; 30 k keys, 64 rows 20 | 22, 128 rows 29 | 23.
+  const long long reads = static_cast<long long>(s.B) * s.Hkv * s.Nk * ((q.Nq + 15) / 16);
+  q.tensor = listed ? C >= 64 : q.Nq > (kv8 ? 16 : 8) && reads >= 131072;
   q.pair = q.tensor && listed && C == 64;
   if (!listed && !q.tensor) q.C = 16;
   q.GQ = (q.Nq + q.C - 1) / q.C;
@@ -187,7 +194,7 @@ struct TopkPlan {
   size_t keys, total;
 };
 constexpr size_t kTopkKeyBytes = size_t{1} << 28;
-constexpr long long kPickWarpRows = 2048;
+
 
 TopkPlan plan_topk(const mcs_block_shape& s, int C, int BK) {
   TopkPlan q{};
@@ -218,10 +225,11 @@ void launch_topk(const TopkParams& p, int kvs, cudaStream_t st) {
   }
   const long long rows = static_cast<long long>(kvs) * p.mc;
   const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-  const bool warps = rows >= kPickWarpRows;  // enough of them to fill the GPU with a warp each
-  if (warps && p.nb <= 8 * 32) launch_dependent(block_pick_warp_kernel<8>, grid, 128, 0, st, p, rows);
-  else if (warps && p.nb <= 16 * 32) launch_dependent(block_pick_warp_kernel<16>, grid, 128, 0, st, p, rows);
-  else if (warps && p.nb <= 32 * 32) launch_dependent(block_pick_warp_kernel<32>, grid, 128, 0, st, p, rows);
+  // a warp a row wherever its keys fit in registers (50 rows of 250: 12.5 us for the whole choice against 13.9
+  // with a CTA a row, 2000 rows of 1000: 52 against 71)
+  if (p.nb <= 8 * 32) launch_dependent(block_pick_warp_kernel<8>, grid, 128, 0, st, p, rows);
+  else if (p.nb <= 16 * 32) launch_dependent(block_pick_warp_kernel<16>, grid, 128, 0, st, p, rows);
+  else if (p.nb <= 32 * 32) launch_dependent(block_pick_warp_kernel<32>, grid, 128, 0, st, p, rows);
   else
     launch_dependent(block_pick_kernel, static_cast<unsigned>(std::min<long long>(rows, 4096)), kTopkThreads,
                      static_cast<size_t>(p.nb) * 8, st, p, rows);
@@ -445,8 +453,9 @@ mcs_status mcs_cache_write(mcs_shape s, const void* K, const void* V, int BK, in
 size_t mcs_block_attn_workspace_size(mcs_block_shape s, int C, int BK, int kb) {
   if (check_block_shape(s) != MCS_OK || !query_rows_ok(C) || !block_rows_ok(BK) || kb < 1 || kb > (s.Nk + BK - 1) / BK)
     return 0;
-  const size_t n = plan_block_attn(s, C, BK, kb, true).total;
-  return kb < (s.Nk + BK - 1) / BK ? n : std::max(n, plan_block_attn(s, C, BK, kb, false).total);
+  const size_t n = plan_block_attn(s, C, BK, kb, true, false).total;
+  if (kb < (s.Nk + BK - 1) / BK) return n;
+  return std::max({n, plan_block_attn(s, C, BK, kb, false, false).total, plan_block_attn(s, C, BK, kb, false, true).total});
 }
 
 mcs_status mcs_block_attn(mcs_block_shape s, const void* Q, const void* K, const void* V, int kv_format,
@@ -481,7 +490,7 @@ mcs_status mcs_block_attn(mcs_block_shape s, const void* Q, const void* K, const
   p.R = static_cast<const __nv_bfloat16*>(R);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
-  const BlockPlan plan = plan_block_attn(s, C, BK, kb, blocks != nullptr);
+  const BlockPlan plan = plan_block_attn(s, C, BK, kb, blocks != nullptr, kv_format != 0);
   p.part = static_cast<float*>(ws);
   p.plse = reinterpret_cast<float*>(static_cast<char*>(ws) + plan.part);
   p.B = s.B;

@@ -371,8 +371,8 @@ __global__ void __launch_bounds__(128) block_pick_warp_kernel(const TopkParams p
 constexpr int kTopkThreads = 256;
 constexpr int kTopkMaxBlocks = 24576;  // keys of a row in shared memory: 8 bytes each
 
-// The same, a CTA a row with its keys in shared memory: longer rows, and few rows (192 rows of 1024: 11.5 us
-// with a warp each).  Two bits a step: the counts of three candidates in one 64-bit sum.
+// The same for longer rows, a CTA a row with its keys in shared memory.  Two bits a step: the counts of three
+// candidates in one 64-bit sum.
 __global__ void __launch_bounds__(kTopkThreads) block_pick_kernel(const TopkParams p, long long rows) {
   extern __shared__ __align__(16) unsigned long long tkeys[];  // nb
   constexpr int WARPS = kTopkThreads / 32;

@@ -253,6 +253,10 @@ SHAPES = [
     (1, 3, 3, 1000, 8192, 64, 64, 64, 100, "holes", None, False),  # many stages, lists of unlike lengths
     (1, 3, 1, 1000, 8192, 128, 64, 32, 200, "holes", [8000], False),
     (2, 2, 2, 1100, 6000, 128, 128, 64, 60, "holes", [6000, 100], False),
+    (2, 6, 2, 3, 33000, 64, 1, 32, 1032, None, [33000, 20001], False),  # whole stores: few rows, and tiles
+    (2, 12, 2, 3, 33000, 128, 16, 64, 516, None, [32999, 64], True),
+    (1, 6, 1, 4, 66000, 64, 64, 128, 516, None, [65999], False),
+    (1, 2, 1, 70, 5000, 64, 1, 32, 157, None, None, True),
 ]
 
 
