@@ -729,6 +729,8 @@ class KVCache:
 
     def __init__(self, B: int, Hkv: int, capacity: int, d: int, BK: int = 64, device=None):
         _block_sizes(BK=BK)
+        if d not in (64, 128) or B < 1 or Hkv < 1:
+            raise ValueError(f"need d of 64 or 128 and at least one batch entry and head, got d = {d}, B = {B}, Hkv = {Hkv}")
         if capacity < 1 or capacity % BK:
             raise ValueError(f"capacity must be a positive multiple of BK = {BK}, got {capacity}")
         dev = "cuda" if device is None else device

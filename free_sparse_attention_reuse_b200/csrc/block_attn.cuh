@@ -165,8 +165,9 @@ __device__ __forceinline__ void e4m3_to_bf16(uint32_t a, uint32_t b, uint32_t* w
 }
 
 // The pipeline of attn_kernel (two softmax streams per tile of 128 query rows, S and O in TMEM, P over
-// S) with the keys of listed blocks in stages of 128: 128 / BK blocks a stage, a TMA box each, or,
-// from an 8-bit store, loaded to registers, widened to bf16 and stored by the four producer warps.
+// S) with the keys of listed blocks in stages of 128: 128 / BK blocks a stage, a TMA box each, or, from an
+// 8-bit store, loaded by bulk copies (warp 13) and widened in shared memory by the four producer warps,
+// keys to fp16 (and Q with them), values to bf16.
 //   PAIR = false  both streams work on the tile's 128 rows, alternate stages; merged at the end.
 //   PAIR = true   lists of 64 rows: stream A takes rows 0-63 with their list, stream B rows 64-127
 //                 with theirs.  The MMAs compute all 128 rows either way; no exponential is spent on

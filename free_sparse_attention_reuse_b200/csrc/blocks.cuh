@@ -134,16 +134,22 @@ __device__ __forceinline__ int candidate_blocks(const TopkParams& p, int kv) {
   return (valid_rows(p.len, kv / p.Hkv, p.Nk) + p.BK - 1) / p.BK;
 }
 
-// 64 rows by 64 blocks a CTA, 8 x 4 a thread, 32 columns of d at a time from shared memory (columns in
-// groups of four, the group's place XORed with its row's so that the transposing stores spread over the
-// banks).  Bound: the fp64 pipe (195 M multiply-adds for 24 heads of 252 x 252 blocks of 128: 11 us at its
-// full rate); 4 x 4 a thread was bound by the reads of shared memory (48 us).
+// D += A B, 8 x 8 x 4, fp64: lane l holds A[l / 4][l % 4], B[l % 4][l / 4] and D[l / 4][2 (l % 4) + {0, 1}].
+__device__ __forceinline__ void mma_f64(double& d0, double& d1, double a, double b) {
+  asm("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0,%1}, {%2}, {%3}, {%0,%1};" : "+d"(d0), "+d"(d1) : "d"(a), "d"(b));
+}
+
+// 64 rows by 64 blocks a CTA on the fp64 tensor cores, 32 x 32 a warp, 32 columns of d at a time from shared
+// memory (rows four doubles longer than that, so that a half warp's fragment reads hit all banks).  Bound:
+// the fp64 pipe (195 M multiply-adds for 24 heads of 252 x 252 blocks of 128: 11 us at its full rate);
+// multiply-adds from 4 x 4 and 8 x 4 values a thread were bound by the reads of shared memory (48, 31 us).
 constexpr int kScoreTile = 64, kScoreDepth = 32, kScoreThreads = 128;
 
 template <int HD>
 __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const TopkParams p) {
-  __shared__ __align__(16) double as[kScoreDepth][kScoreTile], bs[kScoreDepth][kScoreTile];
-  const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
+  __shared__ __align__(16) double as[kScoreTile][kScoreDepth + 4], bs[kScoreTile][kScoreDepth + 4];
+  const int t = threadIdx.x, lane = lane_id(), fr = lane >> 2, fk = lane & 3;
+  const int wm = (warp_id() >> 1) * 32, wn = (warp_id() & 1) * 32;  // this warp's rows and blocks
   const int kv = p.kv0 + blockIdx.z, m0 = blockIdx.y * kScoreTile, j0 = blockIdx.x * kScoreTile;
   const int nv = candidate_blocks(p, kv);
   let_dependents_start();
@@ -151,11 +157,11 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const TopkPa
   if (j0 >= nv) return;
   const size_t row0 = static_cast<size_t>(kv) * p.M + p.m0 + m0;
   const int rows = p.mc - m0;
-  double acc[8][4];
+  double acc[4][4][2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.0;
+    for (int j = 0; j < 4; ++j) acc[i][j][0] = acc[i][j][1] = 0.0;
   float4 a[4], b[4];
   auto load = [&](int k0) {
 #pragma unroll
@@ -182,42 +188,36 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const TopkPa
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = (t >> 3) + 16 * i, k = (t & 7) * 4;
-      const int at = (((r >> 2) ^ (t & 7)) << 2) | (r & 3);
-      as[k][at] = a[i].x, as[k + 1][at] = a[i].y, as[k + 2][at] = a[i].z, as[k + 3][at] = a[i].w;
-      bs[k][at] = b[i].x, bs[k + 1][at] = b[i].y, bs[k + 2][at] = b[i].z, bs[k + 3][at] = b[i].w;
+      *reinterpret_cast<double2*>(&as[r][k]) = make_double2(a[i].x, a[i].y);
+      *reinterpret_cast<double2*>(&as[r][k + 2]) = make_double2(a[i].z, a[i].w);
+      *reinterpret_cast<double2*>(&bs[r][k]) = make_double2(b[i].x, b[i].y);
+      *reinterpret_cast<double2*>(&bs[r][k + 2]) = make_double2(b[i].z, b[i].w);
     }
     __syncthreads();
     if (k0 + kScoreDepth < HD) load(k0 + kScoreDepth);
 #pragma unroll 4
-    for (int k = 0; k < kScoreDepth; ++k) {
-      double x[8], y[4];
-      const int sw = k >> 2;
+    for (int k = 0; k < kScoreDepth; k += 4) {
+      double x[4], y[4];
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const double2 u = *reinterpret_cast<const double2*>(&as[k][(((ty * 2 + (i >> 2)) ^ sw) << 2) + (i & 3)]);
-        x[i] = u.x, x[i + 1] = u.y;
-      }
+      for (int i = 0; i < 4; ++i) x[i] = as[wm + i * 8 + fr][k + fk], y[i] = bs[wn + i * 8 + fr][k + fk];
 #pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        const double2 v = *reinterpret_cast<const double2*>(&bs[k][((tx ^ sw) << 2) + i]);
-        y[i] = v.x, y[i + 1] = v.y;
-      }
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fma(x[i], y[j], acc[i][j]);
+        for (int j = 0; j < 4; ++j) mma_f64(acc[i][j][0], acc[i][j][1], x[i], y[j]);
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = ty * 8 + i;
+  for (int i = 0; i < 4; ++i) {
+    const int r = wm + i * 8 + fr;
     if (r >= rows) continue;
     unsigned long long* out = p.keys + (static_cast<size_t>(blockIdx.z) * p.mc + m0 + r) * p.nb;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = j0 + tx * 4 + j;
-      if (c < nv) out[c] = score_key(acc[i][j]);
-    }
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int c = j0 + wn + j * 8 + fk * 2 + e;
+        if (c < nv) out[c] = score_key(acc[i][j][e]);
+      }
   }
 }
 

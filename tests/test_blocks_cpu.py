@@ -140,6 +140,9 @@ def test_cache_refuses():
     for cap in (0, 100, -64):
         with pytest.raises(ValueError, match="capacity"):
             api.KVCache(1, 2, cap, 64, BK=64, device="cpu")
+    for bad in ((1, 2, 128, 96), (0, 2, 128, 64), (1, 0, 128, 64)):
+        with pytest.raises(ValueError, match="need d"):
+            api.KVCache(*bad, BK=64, device="cpu")
     c = api.KVCache(1, 2, 128, 64, BK=64, device="cpu")
     with pytest.raises(ValueError, match="K must have shape"):
         c.append(bf(1, 1, 4, 64), bf(1, 1, 4, 64))
