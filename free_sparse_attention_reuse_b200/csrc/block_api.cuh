@@ -84,7 +84,6 @@ struct BlockPlan {
   size_t part, total;  // workspace: bytes of the parts' results, and all
 };
 constexpr int kPlanSms = 148;
-constexpr long long kTokenCtas = 888;
 
 BlockPlan plan_block_attn(const mcs_block_shape& s, int C, int BK, int kb, bool listed, bool kv8) {
   BlockPlan q{};
@@ -117,9 +116,13 @@ BlockPlan plan_block_attn(const mcs_block_shape& s, int C, int BK, int kb, bool 
       if (best < 0 || cost < best) best = cost, q.splits = n;
     }
   } else {
-    // enough CTAs to fill the GPU some times over, each with at least 256 keys
+    // Few lists: one wave of CTAs (32 lists of 8 k keys: 13 parts 21 us, 28 parts 25), else two or more, which
+    // evens out lists of unlike lengths (192 lists of 10 k keys, a quarter of them past the end: 2 and 4
+    // parts 97 us, 5 parts 89, 6 parts 94); each part has at least 256 keys.
     const long long keys = static_cast<long long>(kb) * BK;
-    q.splits = static_cast<int>(std::max(1ll, std::min(std::min((kTokenCtas + lists - 1) / lists, keys / 256), 128ll)));
+    const long long wave = kPlanSms * (std::min(q.C, q.Nq) <= 8 ? 3 : 2);
+    const long long n = lists * 4 <= wave ? wave / lists : (2 * wave + lists - 1) / lists;
+    q.splits = static_cast<int>(std::max(1ll, std::min({n, keys / 256, 128ll})));
   }
   const size_t rows = static_cast<size_t>(s.B) * s.H * s.Nq;
   if (q.splits > 1) q.part = round_up(rows * q.splits * s.d * 4, 256);
@@ -155,7 +158,7 @@ mcs_status run_block_attn(const BlockAttnParams& p, cudaStream_t st, int sms) {
   alignas(64) CUtensorMap tmQ, tmK, tmV;
   if (!make_row_map(&tmQ, p.Q, static_cast<uint64_t>(p.B) * p.H * p.Nq, HD, kTile)) return MCS_ERR_CUDA;
   if (KV8) {
-    tmK = tmV = tmQ;  // not used: 8-bit rows are loaded to registers
+    tmK = tmV = tmQ;  // not used: 8-bit rows come by bulk copies
   } else {
     const uint64_t rows = static_cast<uint64_t>(p.B) * p.Hkv * p.Nk;
     if (!make_row_map(&tmK, p.K, rows, HD, p.BK) || !make_row_map(&tmV, p.V, rows, HD, p.BK)) return MCS_ERR_CUDA;

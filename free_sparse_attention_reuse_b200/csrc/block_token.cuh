@@ -89,7 +89,7 @@ struct TokenSmem {
 };
 
 template <int HD, bool KV8, int RT>
-__global__ void __launch_bounds__(kTokenWarps * 32, 2) block_token_kernel(const BlockAttnParams p) {
+__global__ void __launch_bounds__(kTokenWarps * 32, RT == 8 ? 3 : 2) block_token_kernel(const BlockAttnParams p) {
   using L = TokenSmem<HD, KV8>;
   constexpr int KC = L::KC, RING = L::RING;
   constexpr int NT = KC / 8;                     // key tiles
@@ -105,6 +105,8 @@ __global__ void __launch_bounds__(kTokenWarps * 32, 2) block_token_kernel(const 
   __shared__ int sm_valid[kTokenWarps][RING];
   __shared__ float sm_scale[kTokenWarps][RING][2];
   __shared__ int s_end, s_abort;
+  constexpr bool QS = RT == 8 && HD == 128;  // Q's fragments in shared memory: three CTAs an SM instead of two
+  __shared__ __align__(16) uint4 sm_q[QS ? LB * KS / 2 : 1][32];
   float (*sm_o)[RT][HD] = reinterpret_cast<float (*)[RT][HD]>(ring_mem);
 
   let_dependents_start();
@@ -184,6 +186,14 @@ __global__ void __launch_bounds__(kTokenWarps * 32, 2) block_token_kernel(const 
     if constexpr (WIDE) qs1 = q_to_f16<LB * KS * 2>(qb);
   }
 
+  if constexpr (QS) {
+    if (warp == 0)
+#pragma unroll
+      for (int i = 0; i < LB * KS / 2; ++i) sm_q[i][lane] = make_uint4(qa[4 * i], qa[4 * i + 1], qa[4 * i + 2], qa[4 * i + 3]);
+    __syncthreads();
+  }
+  const uint32_t qbase = smem_u32(&sm_q[0][lane]);
+
   const uint8_t* Kb = static_cast<const uint8_t*>(p.K) + static_cast<size_t>(bkv) * p.Nk * L::ROW;
   const uint8_t* Vb = static_cast<const uint8_t*>(p.V) + static_cast<size_t>(bkv) * p.Nk * L::ROW;
   const uint32_t ring = smem_u32(ring_mem) + warp * L::WARP;
@@ -254,6 +264,17 @@ __global__ void __launch_bounds__(kTokenWarps * 32, 2) block_token_kernel(const 
       uint4 kr[NT];
 #pragma unroll
       for (int i = 0; i < NT; ++i) kr[i] = lds16(kbase + (i * 8 + g) * L::ROW + j * 64 + t * 16);
+      uint32_t qf[2 * KS];  // Q's fragments of this load's k steps
+#pragma unroll
+      for (int k = 0; k < KS / 2; ++k) {
+        const int q = j * KS * 2 + 4 * k;
+        if constexpr (QS) {
+          const uint4 u = lds16(qbase + (q / 4) * 512);
+          qf[4 * k] = u.x, qf[4 * k + 1] = u.y, qf[4 * k + 2] = u.z, qf[4 * k + 3] = u.w;
+        } else {
+          qf[4 * k] = qa[q], qf[4 * k + 1] = qa[q + 1], qf[4 * k + 2] = qa[q + 2], qf[4 * k + 3] = qa[q + 3];
+        }
+      }
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         const int q = (j * KS + k) * 2;
@@ -263,8 +284,8 @@ __global__ void __launch_bounds__(kTokenWarps * 32, 2) block_token_kernel(const 
           uint32_t b0, b1;
           if constexpr (KV8) e4m3x4_to_f16(in[k], b0, b1);
           else b0 = in[2 * k], b1 = in[2 * k + 1];
-          if constexpr (WIDE) mma_16816<KV8>(s[i][0], s[i][1], s2[i][0], s2[i][1], qa[q], qb[q], qa[q + 1], qb[q + 1], b0, b1);
-          else mma_8816<KV8>(s[i][0], s[i][1], qa[q], qa[q + 1], b0, b1);
+          if constexpr (WIDE) mma_16816<KV8>(s[i][0], s[i][1], s2[i][0], s2[i][1], qf[2 * k], qb[q], qf[2 * k + 1], qb[q + 1], b0, b1);
+          else mma_8816<KV8>(s[i][0], s[i][1], qf[2 * k], qf[2 * k + 1], b0, b1);
         }
       }
     }
@@ -316,51 +337,57 @@ __global__ void __launch_bounds__(kTokenWarps * 32, 2) block_token_kernel(const 
     // O += P V, 16 keys at a time; 8-bit: O = alpha O + V scale (P V)
 #pragma unroll
     for (int h = 0; h < VH; ++h) {
-      // value rows 16 k + 2 t + {0, 1, 8, 9}: what the lane's P fragments of 16 keys multiply
-      uint32_t vr[NT * 2][4];
-#pragma unroll
-      for (int i = 0; i < NT * 2; ++i) {
+      // value rows 16 k + 2 t + {0, 1, 8, 9}: what the lane's P fragments of 16 keys multiply; 8-bit rows eight
+      // columns at a time
+      auto row_at = [&](int i) {
         const int k = (i >> 2) * 16 + 2 * t + (i & 1) + (i & 2) * 4;
-        const uint32_t a = vbase + k * L::ROW + h * 8 * VB + g * VB;
-        if constexpr (VB == 16) {
-          const uint4 u = lds16(a);
-          vr[i][0] = u.x, vr[i][1] = u.y, vr[i][2] = u.z, vr[i][3] = u.w;
-        } else {
-          asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(vr[i][0]), "=r"(vr[i][1]) : "r"(a));
-        }
-      }
+        return vbase + k * L::ROW + h * 8 * VB + g * VB;
+      };
       if constexpr (KV8) {
 #pragma unroll
-        for (int j = 0; j < VC; j += 2) {
-          const int i = h * VC + j;
-          float c[2][4];
-          // bytes j and j + 1 of two rows side by side, then widened: tiles j and j + 1
-          constexpr uint32_t kSel[2] = {0x5140u, 0x7362u};
-          const uint32_t sel = kSel[(j & 2) >> 1];
+        for (int j8 = 0; j8 < VC; j8 += 8) {
+          uint32_t vr[NT * 2][2];
 #pragma unroll
-          for (int k = 0; k < NT / 2; ++k) {
-            uint32_t b00, b01, b10, b11;
-            e4m3x4_to_f16(__byte_perm(vr[4 * k][j / 4], vr[4 * k + 1][j / 4], sel), b00, b10);
-            e4m3x4_to_f16(__byte_perm(vr[4 * k + 2][j / 4], vr[4 * k + 3][j / 4], sel), b01, b11);
-            if (k == 0) {
-              mma_16816_zero(c[0], pa[k][0], pa[k][1], pa[k][2], pa[k][3], b00, b01);
-              mma_16816_zero(c[1], pa[k][0], pa[k][1], pa[k][2], pa[k][3], b10, b11);
-            } else if constexpr (WIDE) {
-              mma_16816<true>(c[0][0], c[0][1], c[0][2], c[0][3], pa[k][0], pa[k][1], pa[k][2], pa[k][3], b00, b01);
-              mma_16816<true>(c[1][0], c[1][1], c[1][2], c[1][3], pa[k][0], pa[k][1], pa[k][2], pa[k][3], b10, b11);
-            } else {
-              mma_8816<true>(c[0][0], c[0][1], pa[k][0], pa[k][2], b00, b01);
-              mma_8816<true>(c[1][0], c[1][1], pa[k][0], pa[k][2], b10, b11);
+          for (int i = 0; i < NT * 2; ++i)
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(vr[i][0]), "=r"(vr[i][1]) : "r"(row_at(i) + j8));
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            const int i = h * VC + j8 + j;
+            float c[2][4];
+            // bytes j and j + 1 of two rows side by side, then widened: tiles j and j + 1
+            constexpr uint32_t kSel[2] = {0x5140u, 0x7362u};
+            const uint32_t sel = kSel[(j & 2) >> 1];
+#pragma unroll
+            for (int k = 0; k < NT / 2; ++k) {
+              uint32_t b00, b01, b10, b11;
+              e4m3x4_to_f16(__byte_perm(vr[4 * k][j / 4], vr[4 * k + 1][j / 4], sel), b00, b10);
+              e4m3x4_to_f16(__byte_perm(vr[4 * k + 2][j / 4], vr[4 * k + 3][j / 4], sel), b01, b11);
+              if (k == 0) {
+                mma_16816_zero(c[0], pa[k][0], pa[k][1], pa[k][2], pa[k][3], b00, b01);
+                mma_16816_zero(c[1], pa[k][0], pa[k][1], pa[k][2], pa[k][3], b10, b11);
+              } else if constexpr (WIDE) {
+                mma_16816<true>(c[0][0], c[0][1], c[0][2], c[0][3], pa[k][0], pa[k][1], pa[k][2], pa[k][3], b00, b01);
+                mma_16816<true>(c[1][0], c[1][1], c[1][2], c[1][3], pa[k][0], pa[k][1], pa[k][2], pa[k][3], b10, b11);
+              } else {
+                mma_8816<true>(c[0][0], c[0][1], pa[k][0], pa[k][2], b00, b01);
+                mma_8816<true>(c[1][0], c[1][1], pa[k][0], pa[k][2], b10, b11);
+              }
             }
-          }
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            o[i + e][0] = fmaf(c[e][0], vscale, o[i + e][0] * al0), o[i + e][1] = fmaf(c[e][1], vscale, o[i + e][1] * al0);
-            if constexpr (WIDE)
-              o2[i + e][0] = fmaf(c[e][2], vscale, o2[i + e][0] * al1), o2[i + e][1] = fmaf(c[e][3], vscale, o2[i + e][1] * al1);
+            for (int e = 0; e < 2; ++e) {
+              o[i + e][0] = fmaf(c[e][0], vscale, o[i + e][0] * al0), o[i + e][1] = fmaf(c[e][1], vscale, o[i + e][1] * al0);
+              if constexpr (WIDE)
+                o2[i + e][0] = fmaf(c[e][2], vscale, o2[i + e][0] * al1), o2[i + e][1] = fmaf(c[e][3], vscale, o2[i + e][1] * al1);
+            }
           }
         }
       } else {
+        uint32_t vr[NT * 2][4];
+#pragma unroll
+        for (int i = 0; i < NT * 2; ++i) {
+          const uint4 u = lds16(row_at(i));
+          vr[i][0] = u.x, vr[i][1] = u.y, vr[i][2] = u.z, vr[i][3] = u.w;
+        }
 #pragma unroll
         for (int j = 0; j < VC; ++j) {
           const int i = h * VC + j;
