@@ -399,7 +399,7 @@ _blanks: dict = {}
 def _workspace(ws, n: int, t):
     if ws is None:
         if n > 256:
-            return torch.empty(n, dtype=torch.uint8, device=t.device)
+            return t.new_empty(n, dtype=torch.uint8)
         ws = _blanks.get(t.get_device())
         if ws is None:
             ws = _blanks[t.get_device()] = torch.empty(256, dtype=torch.uint8, device=t.device)
@@ -544,8 +544,7 @@ def rotary(q, k, v, pos, axes, theta: float = 10000.0, pairs: str = "adjacent", 
     a, shapes = plan
     _here(q)
     if out is None:
-        dev = q.device
-        out = [None if s is None else torch.empty(s, dtype=torch.bfloat16, device=dev) for s in shapes]
+        out = [None if s is None else q.new_empty(s) for s in shapes]
     else:
         _apart(dict(Q=out[0], K=out[1], V=out[2]), dict(q=q, k=k, v=v, pos=pos, q_weight=q_weight, k_weight=k_weight))
     Q, K, V = out
@@ -572,7 +571,7 @@ def block_means(K, BK: int, kv_len=None, means=None):
     s, shape = plan or _keep(key, _plan_means(K, BK, kv_len, means))
     _here(K)
     if means is None:
-        means = torch.empty(shape, dtype=torch.float32, device=K.device)
+        means = K.new_empty(shape, dtype=torch.float32)
     else:
         _apart(dict(means=means), dict(K=K, kv_len=kv_len))
     check(_lib.load().mcs_block_means(s, _at(K), BK, _at(kv_len), _at(means), _stream(K)), "mcs_block_means")
@@ -610,7 +609,7 @@ def block_topk(Q, means, C: int, kb: int, BK: int, kv_len=None, blocks=None, ws=
     s, shape, n = plan or _keep(key, _plan_topk(Q, means, C, kb, BK, kv_len, blocks))
     _here(Q)
     if blocks is None:
-        blocks = torch.empty(shape, dtype=torch.int32, device=Q.device)
+        blocks = Q.new_empty(shape, dtype=torch.int32)
     else:
         _apart(dict(blocks=blocks), dict(Q=Q, means=means, kv_len=kv_len))
     ws = _workspace(ws, n, Q)
@@ -678,7 +677,7 @@ def block_attn(Q, K, V, blocks, C: int, BK: int, R=None, kv_len=None, k_scale=No
     if out is None:
         out = torch.empty_like(Q)
     if want_lse and lse is None:
-        lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device)
+        lse = Q.new_empty(Q.shape[:3], dtype=torch.float32)
     ws = _workspace(ws, n, Q)
     check(_lib.load().mcs_block_attn(s, _at(Q), _at(K), _at(V), fp8, _at(k_scale), _at(v_scale), _at(blocks), C, BK, kb,
                                      _at(kv_len), _at(R), _at(out), _at(lse), _at(ws), ws.numel(), _stream(Q)),

@@ -769,7 +769,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const StageInfo& info = sInfo[KV8 ? (kv_base + stage_pos(tn, x, i)) % L::INFOS : slot];
             vq[q] = info.valid[r0 + q];
             all &= vq[q];
-            kq[q] = KV8 ? qscale * info.ks[r0 + q] : sl2;
+            // (at least the smallest normal number: masked keys are -inf times this)
+            kq[q] = KV8 ? fmaxf(qscale * info.ks[r0 + q], 1.17549435e-38f) : sl2;
             vsq[q] = KV8 ? info.vs[r0 + q] : 1.f;
           }
           // the QK^T that wrote S has read its K slot: hand the slot back to the producer

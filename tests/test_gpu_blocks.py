@@ -337,6 +337,18 @@ def test_block_attn_infinities_in_valid_keys():
     api.sync_status()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("C,Nq", [(128, 130), (64, 70), (16, 16), (1, 1)])
+@pytest.mark.parametrize("q_size,k_size", [(0.0, 1e-30), (1e-30, 1e-30), (1e-36, 1.0), (1e18, 1e18), (1.0, 0.0)])
+def test_block_attn_tiny_and_large_operands(C, Nq, fp8, q_size, k_size):
+    """Products far under and over one (logits of 0, or one key that takes all), some keys masked."""
+    Nk, BK, d = 320, 64, 64
+    q, k = rnd(40, 1, 2, Nq, d, std=q_size), rnd(41, 1, 2, Nk, d, std=k_size)
+    q[:, :, ::3] = 0
+    run_attn(q, k, rnd(42, 1, 2, Nk, d), None, C, BK, kv=torch.tensor([300], dtype=torch.int32), fp8=fp8,
+             scale=1.0 if q_size < 1e10 else 1e-34)
+
+
 # ------------------------------------------------------------------------------------------ 8-bit store
 @pytest.mark.parametrize("B,H,n,d,BK,start,cap,lens", [
     (1, 2, 256, 64, 64, 0, 256, None), (2, 3, 300, 128, 128, 128, 1024, [300, 17]), (2, 1, 1, 64, 32, 32, 96, [1, 0]),
