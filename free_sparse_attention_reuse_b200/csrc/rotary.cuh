@@ -91,9 +91,10 @@ __device__ __forceinline__ void load_w4(const void* w, int bf16, size_t at, floa
 // pairs in halves a lane holds four elements of the first half and their four partners (two 8-byte
 // pieces), so that nothing is exchanged; lanes beyond the halves hold eight that are not turned.
 // Bound: device memory (480p clip, head norm: 196 us, 92 % of the copy rate; one row in flight and the sines
-// in shared memory left it at 58 %; partners by shuffles left the halves form at 143 us for 403 MB).
+// in shared memory left it at 58 %; partners by shuffles left the halves form at 143 us for 403 MB,
+// three CTAs an SM instead of four at 117 against 105, five at 137).
 template <int HD, int NORM, bool HALVES>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
+__global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(const __grid_constant__ RotaryParams p) {
   constexpr int LPR = HD / 8;                 // lanes of a group
   constexpr int GROUPS = kRotThreads / LPR;   // 16 or 32
   __shared__ float part[2][GROUPS];
