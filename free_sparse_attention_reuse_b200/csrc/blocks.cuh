@@ -483,9 +483,12 @@ __device__ __forceinline__ unsigned quantise4(const float* x, float scale, float
   return lo | (hi << 16);
 }
 
-// NIT: passes of the CTA over a block (its rows / (256 / (HD / 16)), at least 1).
+// One CTA a block, its rows in registers between the maximum and the rounding, so that they are read once.
+// NIT: passes of the CTA over a block (its rows / (256 / (HD / 16)), at least 1).  Bound: device memory (480p
+// clip, 594 MB: 113 us, 80 % of the copy rate), which wants CTAs to overlap: five an SM; four 115 us, three
+// 119, and with a division for every value 187.
 template <int HD, int NIT>
-__global__ void __launch_bounds__(kCacheThreads, 4) cache_write_kernel(const CacheWriteParams p) {
+__global__ void __launch_bounds__(kCacheThreads, 5) cache_write_kernel(const CacheWriteParams p) {
   constexpr int CG = HD / 16;                       // 16-element pieces of a row
   constexpr int RG = kCacheThreads / CG;            // rows of one pass
   constexpr int WARPS = kCacheThreads / 32;
