@@ -392,13 +392,14 @@ def _stream(t):
     return _raw_stream(t.get_device()) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
-# Stands in where a call writes no workspace (one CTA to each list): 256 bytes a device, never touched.
+# Stands in where a call writes no workspace (attention with one CTA to each list): 256 bytes a device, shared by
+# every such call and so never handed to one that writes.
 _blanks: dict = {}
 
 
-def _workspace(ws, n: int, t):
+def _workspace(ws, n: int, t, writes: bool = True):
     if ws is None:
-        if n > 256:
+        if writes:
             return t.new_empty(n, dtype=torch.uint8)
         ws = _blanks.get(t.get_device())
         if ws is None:
@@ -678,7 +679,7 @@ def block_attn(Q, K, V, blocks, C: int, BK: int, R=None, kv_len=None, k_scale=No
         out = torch.empty_like(Q)
     if want_lse and lse is None:
         lse = Q.new_empty(Q.shape[:3], dtype=torch.float32)
-    ws = _workspace(ws, n, Q)
+    ws = _workspace(ws, n, Q, writes=n > 256)  # (256: one part, joined with nothing)
     check(_lib.load().mcs_block_attn(s, _at(Q), _at(K), _at(V), fp8, _at(k_scale), _at(v_scale), _at(blocks), C, BK, kb,
                                      _at(kv_len), _at(R), _at(out), _at(lse), _at(ws), ws.numel(), _stream(Q)),
           "mcs_block_attn")
