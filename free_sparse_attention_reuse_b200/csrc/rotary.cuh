@@ -211,7 +211,8 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(const __grid_con
     for (int i = 0; i < 8; ++i) w[i] = 1.f;
     const void* weights = s < 2 ? p.w[s] : nullptr;
     if (NORM == kNormHead && weights != nullptr) load_w(weights, 0, w);
-    for (int h0 = share; h0 < p.heads[s]; h0 += shares * kRotRows) {
+    // as many passes for every group, for the exchanges inside (a group may have no head in the last)
+    for (int h0 = share; h0 - share < p.heads[s]; h0 += shares * kRotRows) {
       uint4 u[kRotRows];
 #pragma unroll
       for (int k = 0; k < kRotRows; ++k) {

@@ -44,3 +44,20 @@ def test_small_choices_on_two_streams(captured):
     api.sync_status()
     for i in range(2):
         assert torch.equal(got[i].cpu(), want[i].expand(n, -1, -1, -1, -1))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("norm", ["head", "token", None])
+@pytest.mark.parametrize("N,H,Hkv", [(1, 130, 65), (1, 1, 4), (1, 3, 1), (2, 5, 33), (40, 2, 2), (3, 65, 129)])
+def test_rotary_heads_that_do_not_fill_a_warps_groups(N, H, Hkv, norm, d):
+    """Few tokens: a token's heads are shared out over the groups of a warp, which get unlike numbers of them."""
+    def within(got, want, size):
+        assert ((got.cpu().double() - want).abs() <= ref.rotary_bound(want, size)).all()
+
+    q, k = rnd(220, 1, N, H, d), rnd(221, 1, N, Hkv, d)
+    pos = torch.arange(N, dtype=torch.int32)[:, None] * 37 + 5
+    for pairs in ("adjacent", "halves"):
+        (rq, sq), (rk, sk), _ = ref.rotary(q, k, None, pos, (d // 2,), pairs=pairs, norm=norm)
+        Q, K, V = api.rotary(q.to(DEV), k.to(DEV), k.to(DEV), pos.to(DEV), (d // 2,), pairs=pairs, norm=norm)
+        within(Q, rq, sq), within(K, rk, sk)
+        assert torch.equal(V.cpu(), k.transpose(1, 2))
