@@ -204,10 +204,14 @@ __global__ void __launch_bounds__(kTokenWarps * 32, RT == 8 ? 3 : 2) block_token
   auto issue = [&]() {
     const uint32_t slot = issued % RING, dst = ring + slot * 2 * L::RUN;
     ++issued;
-    // masked keys weigh 0, but 0 times what lies in their value rows need not be 0
-    for (int k = valid; k < KC; ++k)
-      for (uint32_t e = lane * 16; e < L::ROW; e += 512)
-        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst + L::RUN + k * L::ROW + e), "r"(0u) : "memory");
+    // masked keys weigh 0, but 0 times what lies in their value rows need not be 0; a later run's copy into these
+    // rows must not pass the stores by
+    if (valid < KC) {
+      for (int k = valid; k < KC; ++k)
+        for (uint32_t e = lane * 16; e < L::ROW; e += 512)
+          asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst + L::RUN + k * L::ROW + e), "r"(0u) : "memory");
+      fence_proxy_async_smem();
+    }
     if (KV8 && lane < 2) {
       const float* src = (lane == 0 ? p.ks : p.vs) + static_cast<size_t>(bkv) * p.nb + blk;
       asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&sm_scale[warp][slot][lane])), "l"(src) : "memory");

@@ -61,3 +61,43 @@ def test_rotary_heads_that_do_not_fill_a_warps_groups(N, H, Hkv, norm, d):
         Q, K, V = api.rotary(q.to(DEV), k.to(DEV), k.to(DEV), pos.to(DEV), (d // 2,), pairs=pairs, norm=norm)
         within(Q, rq, sq), within(K, rk, sk)
         assert torch.equal(V.cpu(), k.transpose(1, 2))
+
+
+def within(got, want, bound):
+    got = got.cpu().double()
+    d = torch.where(got == want, 0.0, (got - want).abs())  # equal infinities
+    assert not d.isnan().any() and bool((d <= bound).all()), f"{float((d - bound).max()):.3e} over the bound"
+
+
+def quantised(k, BK):
+    """(e4m3 values, scales) of [B, H, n, d], n a multiple of BK."""
+    B, H, n, d = k.shape
+    y = k.float().view(B, H, n // BK, BK * d)
+    s = (y.abs().amax(-1) / 448.0).clamp_min(2.0 ** -100)
+    return (y / s[..., None]).view(B, H, n, d).to(torch.float8_e4m3fn), s.contiguous()
+
+
+def attn(q, k, v, ids, C, BK, kv=None, fp8=False, scale=None, r=None):
+    """One call against the plain form."""
+    ks = vs = None
+    if fp8:
+        (k, ks), (v, vs) = quantised(k, BK), quantised(v, BK)
+    want, lse, spread, delta = ref.attn(q, k, v, ids, C, BK, r, kv, ks, vs, scale)
+    on = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    got, gl = api.block_attn(on(q), on(k), on(v), on(ids), C, BK, R=on(r), kv_len=on(kv), k_scale=on(ks), v_scale=on(vs),
+                             want_lse=True, scale=scale)
+    within(got, want, ref.attn_bound(want, spread, delta))
+    within(gl, lse, ref.lse_bound(lse.nan_to_num(neginf=0.0), delta))
+    return got
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d,BK,C", [(64, 32, 1), (128, 32, 16), (64, 128, 16), (128, 64, 1)])
+def test_cut_block_between_whole_ones(d, BK, C, fp8):
+    """A block that ends at the length, named again and again between whole ones: its cleared rows are filled anew."""
+    nb = 6
+    kv = torch.tensor([nb * BK - 5], dtype=torch.int32)
+    q, k, v = rnd(230, 1, 2, C, d), rnd(231, 1, 1, nb * BK, d), rnd(232, 1, 1, nb * BK, d)
+    for ids in ([5, 0, 5, 1, 5, 2], [5, 5, 5, 0, 1, 2], [0, 5, 3, 4, 5, 5]):
+        attn(q, k, v, torch.tensor(ids, dtype=torch.int32).expand(1, 2, 1, nb).contiguous(), C, BK, kv, fp8)
+    api.sync_status()
