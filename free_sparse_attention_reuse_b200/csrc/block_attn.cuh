@@ -438,14 +438,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             ++issued;
           }
         }
-        if (!okp) {
-          // after an abort, the copies already issued land before the CTA releases its shared memory (on
-          // a normal exit every one has been consumed)
-          if (q_issued > 0) mbar_drain(q_full, (q_issued - 1) & 1);
-          for (uint32_t s = 0; s < ring && s < issued; ++s) {
-            const uint32_t last = issued - 1 - ((issued - 1 + ring - s) % ring);
-            mbar_drain(full + s, (last / ring) & 1);
-          }
+        // the copies issued land before the CTA releases its shared memory (consumed, and so at once, unless a
+        // wait of some role ran out: this warp need not have noticed)
+        if (q_issued > 0) mbar_drain(q_full, (q_issued - 1) & 1);
+        for (uint32_t s = 0; s < ring && s < issued; ++s) {
+          const uint32_t last = issued - 1 - ((issued - 1 + ring - s) % ring);
+          mbar_drain(full + s, (last / ring) & 1);
         }
       }
     } else {
@@ -721,12 +719,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (ok && t + 1 < T) look(t + 1);
           }
         }
-        if (*abort_flag) {  // the copies under way land before the CTA releases its shared memory
-          if (u_it > 0) mbar_drain(q_full, (u_it - 1) & 1);
-          for (uint32_t s = 0; s < RAWS && s < raw; ++s) {
-            const uint32_t last = raw - 1 - ((raw - 1 + RAWS - s) % RAWS);
-            mbar_drain(raw_full + s, (last / RAWS) & 1);
-          }
+        // the copies issued land before the CTA releases its shared memory, whatever the other roles did
+        if (u_it > 0) mbar_drain(q_full, (u_it - 1) & 1);
+        for (uint32_t s = 0; s < RAWS && s < raw; ++s) {
+          const uint32_t last = raw - 1 - ((raw - 1 + RAWS - s) % RAWS);
+          mbar_drain(raw_full + s, (last / RAWS) & 1);
         }
       }
     }  // the other warps only complete the warpgroup

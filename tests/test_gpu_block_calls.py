@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import block_reference as ref
-from free_sparse_attention_reuse_b200 import api
+from free_sparse_attention_reuse_b200 import _lib, api
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -101,3 +101,36 @@ def test_cut_block_between_whole_ones(d, BK, C, fp8):
     for ids in ([5, 0, 5, 1, 5, 2], [5, 5, 5, 0, 1, 2], [0, 5, 3, 4, 5, 5]):
         attn(q, k, v, torch.tensor(ids, dtype=torch.int32).expand(1, 2, 1, nb).contiguous(), C, BK, kv, fp8)
     api.sync_status()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("C,Nq,kb", [(128, 700, 3), (64, 700, 1), (64, 100, 200), (16, 32, 40)])
+def test_waits_given_up_at_once(C, Nq, kb, d, fp8):
+    """No patience at all: a role may give up while copies are under way that another one issued.  They land before
+    the CTA ends, the call is reported or right, and so is the next."""
+    Nk, BK = 16384, 64
+    q, k, v = rnd(240, 1, 2, Nq, d).to(DEV), rnd(241, 1, 2, Nk, d), rnd(242, 1, 2, Nk, d)
+    kw = {}
+    if fp8:
+        (k, ks), (v, vs) = quantised(k, BK), quantised(v, BK)
+        kw = dict(k_scale=ks.to(DEV), v_scale=vs.to(DEV))
+    k, v = k.to(DEV), v.to(DEV)
+    ids = torch.rand(1, 2, -(-Nq // C), Nk // BK, generator=torch.Generator().manual_seed(243)).topk(kb, -1).indices
+    ids = ids.int().to(DEV)
+    want = api.block_attn(q, k, v, ids, C, BK, want_lse=True, **kw)
+    api.sync_status()
+    for _ in range(5):
+        _lib.load().mcs_set_attn_wait_limit(1, None)
+        try:
+            got = api.block_attn(q, k, v, ids, C, BK, want_lse=True, **kw)
+            try:
+                api.sync_status()
+                assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+            except _lib.MCSError as e:
+                assert e.status == 7
+        finally:
+            _lib.load().mcs_set_attn_wait_limit(0, None)
+        got = api.block_attn(q, k, v, ids, C, BK, want_lse=True, **kw)
+        api.sync_status()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
