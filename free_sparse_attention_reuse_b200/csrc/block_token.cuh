@@ -179,7 +179,11 @@ __global__ void __launch_bounds__(kTokenWarps * 32, RT == 8 ? 3 : 2) block_token
   }
 
   // 8-bit rows are widened to fp16 (one instruction for two values; bf16 takes four), so Q is fp16 as well,
-  // and P, which is at most 1; the V scale is applied to a run's products in fp32.
+  // and P.  fp16 ends at 2^-24 and is rounded coarser from 2^-14 down, while a key of little weight may have
+  // the largest value: P, at most 1, is multiplied by 2^15, so that it is off by at most 2^-11 of itself down to
+  // 2^-29 of the row's largest and by 2^-40 of that below.  The V scale is applied to a run's products in
+  // fp32, and takes the 2^15 back.
+  constexpr float kPUp = 32768.f;
   float qs0 = 1.f, qs1 = 1.f;
   if constexpr (KV8) {
     qs0 = q_to_f16<LB * KS * 2>(qa);
@@ -254,7 +258,7 @@ __global__ void __launch_bounds__(kTokenWarps * 32, RT == 8 ? 3 : 2) block_token
     }
     const uint32_t kbase = ring + slot * 2 * L::RUN, vbase = kbase + L::RUN;
     const int nvalid = sm_valid[warp][slot];
-    const float ks = KV8 ? sm_scale[warp][slot][0] : 1.f, vscale = KV8 ? sm_scale[warp][slot][1] : 1.f;
+    const float ks = KV8 ? sm_scale[warp][slot][0] : 1.f, vscale = KV8 ? sm_scale[warp][slot][1] * (1.f / kPUp) : 1.f;
     const float ks0 = p.scale_log2 * ks * qs0, ks1 = p.scale_log2 * ks * qs1;
     float s[NT][2], s2[WIDE ? NT : 1][2];
 #pragma unroll
@@ -326,7 +330,7 @@ __global__ void __launch_bounds__(kTokenWarps * 32, RT == 8 ? 3 : 2) block_token
     uint32_t pa[NT / 2][4];
 #pragma unroll
     for (int k = 0; k < NT / 2; ++k) {
-      auto frag = [&](const float* x) { return KV8 ? pack_f16x2(x[0], x[1]) : pack_bf16x2(x[0], x[1]); };
+      auto frag = [&](const float* x) { return KV8 ? pack_f16x2(x[0] * kPUp, x[1] * kPUp) : pack_bf16x2(x[0], x[1]); };
       pa[k][0] = frag(s[2 * k]), pa[k][2] = frag(s[2 * k + 1]);
       pa[k][1] = pa[k][3] = 0;
       if constexpr (WIDE) pa[k][1] = frag(s2[2 * k]), pa[k][3] = frag(s2[2 * k + 1]);

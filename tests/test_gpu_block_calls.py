@@ -134,3 +134,18 @@ def test_waits_given_up_at_once(C, Nq, kb, d, fp8):
         got = api.block_attn(q, k, v, ids, C, BK, want_lse=True, **kw)
         api.sync_status()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("C,Nq", [(1, 1), (1, 6), (16, 16), (128, 130), (64, 70)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("gap,smaller", [(12, 256), (14, 256), (16, 4096), (20, 65536), (24, 2 ** 20)])
+def test_first_key_takes_the_weight_but_its_value_is_small(gap, smaller, d, C, Nq):
+    """8 bits: the other keys' probabilities are around e^-gap, yet their values make the result."""
+    Nk, BK = 512, 32
+    q, k, v = torch.zeros(1, 1, Nq, d), 0.05 * torch.randn(1, 1, Nk, d, generator=torch.Generator().manual_seed(250)), rnd(251, 1, 1, Nk, d)
+    q[..., 0] = 8.0
+    k[0, 0, :, 0] = 0.0
+    k[0, 0, 0, 0] = gap / 8.0
+    v[:, :, :BK] /= smaller
+    attn(q.bfloat16(), k.bfloat16(), v.abs(), None, C, BK, fp8=True, scale=1.0)
+    api.sync_status()
