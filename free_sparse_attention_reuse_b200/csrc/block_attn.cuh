@@ -850,15 +850,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             chunk_exps(sr + 32 * q, kq[q], vsq[q], m_used == -INFINITY ? 0.f : m_used, pk, cs);
             const bool big = !(cs.x + cs.y <= 4294967296.f);  // 2^32, or inf / NaN
             if (__builtin_expect(__any_sync(0xffffffffu, big), 0)) {
-              // rare: raise this row's reference to the run's largest logit by whole octaves (so that
-              // rescaling bf16 P is exact), rescale what is behind it, and redo the run
+              // rare: raise this row's reference to the run's largest logit, by whole octaves where anything is
+              // left of what is behind it (so that rescaling bf16 P is exact), rescale that, and redo the run with
+              // its products rounded as the reference is: no key of it lies above its largest then, however
+              // large they are
               const float mz = m_used == -INFINITY ? 0.f : m_used;
-              float xm = -INFINITY;
+              float top = -INFINITY;
 #pragma unroll
-              for (int c = 0; c < 32; ++c) xm = fmaxf(xm, fmaf(__uint_as_float(sr[32 * q + c]), kq[q], -mz));
-              const bool raise = big && xm > 0.f;
-              const float xr = raise ? fminf(ceilf(xm), 65536.f) : 0.f;
-              const int n = static_cast<int>(xr);
+              for (int c = 0; c < 32; ++c) {
+                const float s = __fmul_rn(__uint_as_float(sr[32 * q + c]), kq[q]);
+                top = fmaxf(top, s);
+                sr[32 * q + c] = __float_as_uint(s);
+              }
+              const bool raise = big && top > mz;
+              const float xr = raise ? ceilf(top - mz) : 0.f;
+              const int n = static_cast<int>(fminf(xr, 127.f));
               const float alpha = n >= 127 ? 0.f : __int_as_float((127 - n) << 23);  // 2^-n
               if (!SUB && q >= kPSplit && !o_lo) {
                 if (!mbar_wait_warp(pvlo_done + x, sc & 1, abort_flag, wl)) { ok = false; break; }
@@ -887,8 +893,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 tmem_st16(tS + 16 * q2, pv);
               }
               tmem_st_wait();
-              if (raise) m_used = mz + xr;
-              chunk_exps(sr + 32 * q, kq[q], vsq[q], m_used == -INFINITY ? 0.f : m_used, pk, cs);
+              if (raise) m_used = n >= 127 ? top : mz + xr;
+              chunk_exps(sr + 32 * q, 1.f, vsq[q], m_used == -INFINITY ? 0.f : m_used, pk, cs);
             }
             rs = __fadd2_rn(rs, cs);
             tmem_st16(tS + 16 * q, pk);

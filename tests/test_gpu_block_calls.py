@@ -149,3 +149,21 @@ def test_first_key_takes_the_weight_but_its_value_is_small(gap, smaller, d, C, N
     v[:, :, :BK] /= smaller
     attn(q.bfloat16(), k.bfloat16(), v.abs(), None, C, BK, fp8=True, scale=1.0)
     api.sync_status()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("C,Nq", [(128, 200), (64, 200), (16, 16), (1, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [40.0, 2000.0, 1e6, 1e8])
+def test_logits_far_apart(size, d, C, Nq, fp8):
+    """Later keys above the first ones by up to 1e9 octaves, and rows that fall as far: one key takes all."""
+    Nk, BK = 1024, 64
+    q, k, v = torch.zeros(1, 2, Nq, d), rnd(260, 1, 2, Nk, d).float(), rnd(261, 1, 2, Nk, d)
+    q[..., 0] = 16.0
+    q[:, 1, ::2, 0] = -16.0
+    k[..., 0] = torch.where(torch.arange(Nk) < 500, -size, size) + torch.arange(Nk) * size / 4096
+    q, k = q.bfloat16(), k.bfloat16()
+    attn(q, k, v, None, C, BK, fp8=fp8, scale=1.0)
+    ids = torch.arange(Nk // BK, dtype=torch.int32).expand(1, 2, -(-Nq // C), -1).contiguous()
+    attn(q, k, v, ids, C, BK, fp8=fp8, scale=1.0)
+    api.sync_status()
