@@ -360,7 +360,7 @@ _plans: dict = {}
 def _lookup(*rest, tensors):
     """(key, plan) of a call: what the checks look at, hashable, and what passed for it before.  The key is
     None for a call that the checks have to see (an argument that is no tensor, or that cannot be a key)."""
-    try:
+    try:  # (`rest` holds numbers, strings and tuples of them: a tensor is equal to itself whatever it holds)
         k = rest + tuple([None if t is None else (t.dtype, t.shape, t.is_contiguous(), t.get_device()) for t in tensors])
         return k, _plans.get(k)
     except (AttributeError, TypeError):
@@ -456,6 +456,11 @@ def _length(t, name: str, B: int):
         _spec(t, name, torch.int32, (B,))
 
 
+def _number(x):
+    """A scalar argument as a float: what a call is known by later has to be its value."""
+    return None if x is None else float(x)
+
+
 def _plan_rotary(q, k, v, pos, axes, theta, pairs, norm, q_weight, k_weight, eps, out):
     if pairs not in ("adjacent", "halves"):
         raise ValueError(f"pairs must be 'adjacent' or 'halves', got {pairs!r}")
@@ -480,7 +485,6 @@ def _plan_rotary(q, k, v, pos, axes, theta, pairs, norm, q_weight, k_weight, eps
             raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
         if t.stride(3) != 1 or any(x % 8 for x in _strides(t)):
             raise ValueError(f"{name} must have consecutive elements in a row and strides that are multiples of 8")
-    axes = tuple(int(a) for a in axes)
     if not 1 <= len(axes) <= 4 or any(a < 2 or a % 2 for a in axes) or sum(axes) > d:
         raise ValueError(f"axes must be one to four even sizes of at most {d} in all, got {axes}")
     if pairs == "halves" and sum(axes) % 16:
@@ -536,10 +540,12 @@ def rotary(q, k, v, pos, axes, theta: float = 10000.0, pairs: str = "adjacent", 
     None, "head" (over a row, weights [d]) or "token" (over all heads of a token, weights
     [heads, d]); weights fp32 or bf16, or None for ones.  Returns Q [B, H, N, d], K and V
     [B, Hkv, N, d] contiguous (None where the input is None); out = (Q, K, V) to reuse buffers."""
-    key = plan = None
-    if type(axes) is tuple:  # (q, k and v are views: their strides count)
-        key, plan = _lookup("rotary", axes, theta, pairs, norm, eps, *[t.stride() for t in (q, k, v) if isinstance(t, torch.Tensor)],
-                            tensors=(q, k, v, pos, q_weight, k_weight, *(out or ())))
+    given, axes, theta, eps = tuple(axes), tuple(map(int, axes)), _number(theta), _number(eps)
+    if given != axes:
+        raise ValueError(f"axes must be whole numbers, got {given}")
+    # (q, k and v are views: their strides count)
+    key, plan = _lookup("rotary", axes, theta, pairs, norm, eps, *[t.stride() for t in (q, k, v) if isinstance(t, torch.Tensor)],
+                        tensors=(q, k, v, pos, q_weight, k_weight, *(out or ())))
     if plan is None:
         plan = _keep(key, _plan_rotary(q, k, v, pos, axes, theta, pairs, norm, q_weight, k_weight, eps, out))
     a, shapes = plan
@@ -653,7 +659,7 @@ def _plan_block_attn(Q, K, V, blocks, C, BK, R, kv_len, k_scale, v_scale, out, l
     if lse is not None:
         _spec(lse, "lse", torch.float32, (B, H, Nq))
     _on_device(Q=Q, K=K, V=V, blocks=blocks, R=R, kv_len=kv_len, k_scale=k_scale, v_scale=v_scale, out=out, lse=lse)
-    s = _lib.BlockShape(B, H, Hkv, Nq, Nk, d, 0.0 if scale is None else float(scale))
+    s = _lib.BlockShape(B, H, Hkv, Nq, Nk, d, 0.0 if scale is None else scale)
     n = int(_lib.load().mcs_block_attn_workspace_size(s, C, BK, kb))
     if n == 0:
         raise _lib.MCSError(2, "mcs_block_attn_workspace_size: invalid shape")
@@ -669,6 +675,7 @@ def block_attn(Q, K, V, blocks, C: int, BK: int, R=None, kv_len=None, k_scale=No
     [B, Hkv, Nk / BK].  blocks: int32 [B, H, ceil(Nq / C), kb] (a list ends at its first negative
     entry), or None for every block.  kv_len: int32 [B], valid keys of each batch entry.  R: bf16
     like Q, added to the result.  A row without a key gives R (0 without R) and lse = -inf."""
+    scale = _number(scale)
     key, plan = _lookup("attn", C, BK, scale, tensors=(Q, K, V, blocks, R, kv_len, k_scale, v_scale, out, lse))
     s, kb, n, fp8 = plan or _keep(key, _plan_block_attn(Q, K, V, blocks, C, BK, R, kv_len, k_scale, v_scale,
                                                                    out, lse, scale))

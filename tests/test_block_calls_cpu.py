@@ -53,3 +53,29 @@ def test_choice_never_writes_to_a_shared_workspace(rec, H, nb, C):
     name, args = rec.calls[-1]
     assert name == "mcs_block_topk" and args[8] not in shared
     assert args[9] == rec.lib.mcs_block_topk_workspace_size(_lib.BlockShape(1, H, H, 1, 32 * nb, 64, 0.0), C, 32)
+
+
+def test_scalar_arguments_count_by_value(rec):
+    """A tensor (or array) as a scalar argument, changed in place between two calls of the same shapes."""
+    q, k, ids = bf(1, 2, 64, 64), bf(1, 2, 64, 64), torch.zeros(1, 2, 1, 1, dtype=torch.int32)
+    scale = torch.tensor(0.5)
+    for x in (0.5, 0.25):
+        scale.fill_(x)
+        api.block_attn(q, k, k, ids, 64, 32, scale=scale)
+        assert rec.calls[-1][1][0].scale == x
+    theta, eps = torch.tensor(100.0), torch.tensor(0.5)
+    axis, pos = torch.tensor(32), torch.zeros(64, 2, dtype=torch.int32)
+    for x in (0.5, 0.25):
+        eps.fill_(x), theta.fill_(200 * x), axis.fill_(int(64 * x))
+        api.rotary(q.transpose(1, 2), None, None, pos, (axis, 16), theta=theta, eps=eps, norm="head")
+        a = rec.calls[-1][1][0]
+        assert a.eps == x and a.theta == 200 * x and a.axis_dim[0] == int(64 * x)
+    for key in api._plans:
+        assert not any(isinstance(x, torch.Tensor) for part in key for x in (part if isinstance(part, tuple) else (part,)))
+
+
+@pytest.mark.parametrize("axes", [(32.5, 16), [16, 15.5]])
+def test_axes_that_are_no_whole_numbers(rec, axes):
+    q = bf(1, 64, 2, 64)
+    with pytest.raises(ValueError, match="whole"):
+        api.rotary(q, None, None, torch.zeros(64, 2, dtype=torch.int32), axes)
