@@ -436,19 +436,21 @@ def _strides(t):
 
 
 def _apart(outs: dict, ins: dict):
-    """No output that the caller gives may share memory with an input: inputs are read after outputs
-    have been written."""
+    """No output that the caller gives may share memory with an input or with another output: inputs are read
+    after outputs have been written, and outputs are written in any order."""
     def span(t):
         n = 1 + sum((s - 1) * st for s, st in zip(t.shape, t.stride())) if t.numel() else 0
         return t.data_ptr(), t.data_ptr() + n * t.element_size()
 
-    for a, o in outs.items():
-        if o is None:
+    held = [(name, *span(t)) for name, t in ins.items() if t is not None]
+    for name, t in outs.items():
+        if t is None:
             continue
-        lo, hi = span(o)
-        for b, t in ins.items():
-            if t is not None and lo < span(t)[1] and span(t)[0] < hi:
-                raise ValueError(f"{a} must not share memory with {b}")
+        lo, hi = span(t)
+        for other, a, b in held:
+            if lo < b and a < hi:
+                raise ValueError(f"{name} must not share memory with {other}")
+        held.append((name, lo, hi))
 
 
 def _length(t, name: str, B: int):
@@ -508,6 +510,8 @@ def _plan_rotary(q, k, v, pos, axes, theta, pairs, norm, q_weight, k_weight, eps
         _spec(w, name, wdt, (d,) if norm == "head" else (heads, d))
     shapes = [(B, H, N, d), None if k is None else (B, Hkv, N, d), None if v is None else (B, Hkv, N, d)]
     if out is not None:
+        if len(out) != 3:
+            raise ValueError(f"out must be (Q, K, V), got {len(out)} of them")
         for o, shape, name in zip(out, shapes, ("Q", "K", "V")):
             if (o is None) != (shape is None):
                 raise ValueError(f"{name} must be given exactly where its input is")
@@ -615,11 +619,11 @@ def block_topk(Q, means, C: int, kb: int, BK: int, kv_len=None, blocks=None, ws=
     key, plan = _lookup("topk", C, kb, BK, tensors=(Q, means, kv_len, blocks))
     s, shape, n = plan or _keep(key, _plan_topk(Q, means, C, kb, BK, kv_len, blocks))
     _here(Q)
+    own, ws = ws is None, _workspace(ws, n, Q)
+    if blocks is not None or not own:
+        _apart(dict(blocks=blocks, ws=None if own else ws), dict(Q=Q, means=means, kv_len=kv_len))
     if blocks is None:
         blocks = Q.new_empty(shape, dtype=torch.int32)
-    else:
-        _apart(dict(blocks=blocks), dict(Q=Q, means=means, kv_len=kv_len))
-    ws = _workspace(ws, n, Q)
     check(_lib.load().mcs_block_topk(s, _at(Q), _at(means), C, BK, kb, _at(kv_len), _at(blocks), _at(ws), ws.numel(),
                                      _stream(Q)), "mcs_block_topk")
     return blocks
@@ -680,13 +684,13 @@ def block_attn(Q, K, V, blocks, C: int, BK: int, R=None, kv_len=None, k_scale=No
     s, kb, n, fp8 = plan or _keep(key, _plan_block_attn(Q, K, V, blocks, C, BK, R, kv_len, k_scale, v_scale,
                                                                    out, lse, scale))
     _here(Q)
-    if out is not None or lse is not None:
-        _apart(dict(out=out, lse=lse), dict(Q=Q, K=K, V=V, R=R, blocks=blocks, kv_len=kv_len, k_scale=k_scale, v_scale=v_scale))
+    own, ws = ws is None, _workspace(ws, n, Q, writes=n > 256)  # (256: one part, joined with nothing)
+    if out is not None or lse is not None or not own:
+        _apart(dict(out=out, lse=lse, ws=None if own else ws), dict(Q=Q, K=K, V=V, R=R, blocks=blocks, kv_len=kv_len, k_scale=k_scale, v_scale=v_scale))
     if out is None:
         out = torch.empty_like(Q)
     if want_lse and lse is None:
         lse = Q.new_empty(Q.shape[:3], dtype=torch.float32)
-    ws = _workspace(ws, n, Q, writes=n > 256)  # (256: one part, joined with nothing)
     check(_lib.load().mcs_block_attn(s, _at(Q), _at(K), _at(V), fp8, _at(k_scale), _at(v_scale), _at(blocks), C, BK, kb,
                                      _at(kv_len), _at(R), _at(out), _at(lse), _at(ws), ws.numel(), _stream(Q)),
           "mcs_block_attn")
@@ -717,12 +721,15 @@ def cache_write(K, V, K8, V8, k_scale, v_scale, BK: int, start: int = 0, means=N
     [B, H, capacity / BK]), and each block's mean key into means (fp32 [B, H, capacity / BK, d]) if
     given.  start and capacity are multiples of BK; a block's scale comes from this call's rows, so an
     unfinished block is lengthened by writing its rows again.  lens: int32 [B], valid rows of this
-    call; rows behind them stay as they were."""
+    call; rows behind them stay as they were.  No output may share memory with another or with an input."""
     key, plan = _lookup("write", BK, start, tensors=(K, V, K8, V8, k_scale, v_scale, means, lens))
     s, cap = plan or _keep(key, _plan_write(K, V, K8, V8, k_scale, v_scale, BK, start, means, lens))
     _here(K)
-    check(_lib.load().mcs_cache_write(s, _at(K), _at(V), BK, start, cap, _at(lens), _at(K8), _at(V8), _at(k_scale),
-                                      _at(v_scale), _at(means), _stream(K)), "mcs_cache_write")
+    status = _lib.load().mcs_cache_write(s, _at(K), _at(V), BK, start, cap, _at(lens), _at(K8), _at(V8), _at(k_scale),
+                                         _at(v_scale), _at(means), _stream(K))
+    if status == 1:  # (looked at there, where it costs nothing; here to say which)
+        _apart(dict(K8=K8, V8=V8, k_scale=k_scale, v_scale=v_scale, means=means), dict(K=K, V=V, lens=lens))
+    check(status, "mcs_cache_write")
 
 
 class KVCache:

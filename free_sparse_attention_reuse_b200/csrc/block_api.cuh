@@ -35,6 +35,20 @@ void launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned threads, si
   cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 
+// Does the first span of bytes share any with one of the others?  (The CTAs of a call write in any order.)
+struct Span {
+  const void* p;  // NULL: none
+  size_t bytes;
+};
+bool shares(const Span& a, std::initializer_list<Span> others) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(a.p), hi = lo + a.bytes;
+  for (const Span& o : others) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(o.p);
+    if (a.p != nullptr && o.p != nullptr && lo < x + o.bytes && x < hi) return true;
+  }
+  return false;
+}
+
 bool block_rows_ok(int BK) { return BK == 32 || BK == 64 || BK == 128; }
 bool query_rows_ok(int C) { return C == 1 || C == 16 || C == 64 || C == 128; }
 
@@ -420,6 +434,15 @@ mcs_status mcs_cache_write(mcs_shape s, const void* K, const void* V, int BK, in
   if (!aligned16(K) || !aligned16(V) || !aligned16(K8) || !aligned16(V8) || !aligned16(k_scale) || !aligned16(v_scale) ||
       (means && !aligned16(means)) || (reinterpret_cast<uintptr_t>(len) & 3u))
     return MCS_ERR_DTYPE_ALIGN;
+  {
+    const size_t heads = static_cast<size_t>(s.B) * s.H, blocks = heads * (capacity / BK);
+    const Span k{K, heads * s.N * s.d * 2}, v{V, k.bytes}, l{len, static_cast<size_t>(s.B) * 4};
+    const Span k8{K8, heads * capacity * s.d}, v8{V8, k8.bytes}, ks{k_scale, blocks * 4}, vs{v_scale, ks.bytes};
+    const Span m{means, blocks * s.d * 4};
+    if (shares(k8, {k, v, l, v8, ks, vs, m}) || shares(v8, {k, v, l, ks, vs, m}) || shares(ks, {k, v, l, vs, m}) ||
+        shares(vs, {k, v, l, m}) || shares(m, {k, v, l}))
+      return MCS_ERR_INVALID_ARG;
+  }
   DeviceInfo* di = nullptr;
   if ((e = block_device(&di)) != MCS_OK) return e;
   CacheWriteParams p{};

@@ -283,7 +283,8 @@ mcs_status mcs_block_topk(mcs_block_shape s, const void* Q, const float* means, 
  * [B, H, capacity / BK, d]) gets the mean of each block's keys before rounding, as mcs_block_means.
  * start and capacity are multiples of BK (a block is written whole: to lengthen an unfinished one, write its
  * rows again).  len (nullable, int32 [B]): valid rows of this call for each batch entry; rows behind them,
- * and blocks without a valid row, stay as they were. */
+ * and blocks without a valid row, stay as they were.  An output that shares memory with another or with an
+ * input is MCS_ERR_INVALID_ARG. */
 mcs_status mcs_cache_write(mcs_shape s, const void* K, const void* V, int BK, int start, int capacity,
                            const int32_t* len, void* K8, void* V8, float* k_scale, float* v_scale, float* means,
                            void* stream);

@@ -79,3 +79,59 @@ def test_axes_that_are_no_whole_numbers(rec, axes):
     q = bf(1, 64, 2, 64)
     with pytest.raises(ValueError, match="whole"):
         api.rotary(q, None, None, torch.zeros(64, 2, dtype=torch.int32), axes)
+
+
+def store(B=1, H=2, cap=128, d=64, BK=32):
+    e4m3 = lambda: torch.zeros(B, H, cap, d).to(torch.float8_e4m3fn)  # noqa: E731
+    return dict(K=bf(B, H, 64, d), V=bf(B, H, 64, d), K8=e4m3(), V8=e4m3(), ks=torch.zeros(B, H, cap // BK),
+                vs=torch.zeros(B, H, cap // BK), means=torch.zeros(B, H, cap // BK, d))
+
+
+def overlay(t, other):
+    """A tensor like t that lies over the memory of `other` (as far as it goes)."""
+    flat = other.view(torch.uint8).flatten()
+    return flat[:t.numel() * t.element_size()].view(t.dtype).view(t.shape)
+
+
+@pytest.mark.parametrize("a,b", [("V8", "K8"), ("K8", "means"), ("ks", "vs"), ("vs", "K8"), ("ks", "means"), ("means", "V8"),
+                                 ("K8", "K"), ("V8", "V"), ("vs", "V"), ("means", "K"), ("lens", "ks"), ("lens", "K8")])
+def test_store_in_overlapping_memory(rec, monkeypatch, a, b):
+    big = torch.zeros(1 << 16, dtype=torch.uint8)
+    t = store()
+    t["lens"] = torch.zeros(1, dtype=torch.int32)
+    t[b] = overlay(t[b], big)
+    t[a] = overlay(t[a], big)
+    monkeypatch.setattr(Recorder, "LAUNCHES", ())  # the library's own check, which comes before any launch
+    with pytest.raises(ValueError, match="share"):
+        api.cache_write(t["K"], t["V"], t["K8"], t["V8"], t["ks"], t["vs"], 32, means=t["means"], lens=t["lens"])
+
+
+def test_store_side_by_side_in_one_buffer(rec):
+    """Parts of one buffer that touch do not share memory."""
+    t = store()
+    buf, at = torch.zeros(1 << 16, dtype=torch.uint8), 0
+    for n in ("K8", "V8", "ks", "vs", "means"):
+        x = t[n]
+        t[n] = overlay(x, buf[at:])
+        at += x.numel() * x.element_size()
+    api.cache_write(t["K"], t["V"], t["K8"], t["V8"], t["ks"], t["vs"], 32, means=t["means"])
+    api._apart({n: t[n] for n in ("K8", "V8", "ks", "vs", "means")}, dict(K=t["K"], V=t["V"]))
+    assert rec.calls[-1][0] == "mcs_cache_write"
+
+
+def test_outputs_apart_from_each_other(rec):
+    x, pos = bf(1, 8, 2, 64), torch.zeros(8, 1, dtype=torch.int32)
+    o = bf(1, 2, 8, 64)
+    with pytest.raises(ValueError, match="share"):
+        api.rotary(x, x, None, pos, (64,), out=(o, o, None))
+    with pytest.raises(ValueError, match="of them"):
+        api.rotary(x, None, None, pos, (64,), out=(o, None))
+    q, k = bf(1, 2, 64, 64), bf(1, 2, 64, 64)
+    out, ids = bf(1, 2, 64, 64), torch.zeros(1, 2, 1, 1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="share"):
+        api.block_attn(q, k, k, ids, 64, 32, out=out, lse=overlay(torch.zeros(1, 2, 64), out))
+    with pytest.raises(ValueError, match="share"):
+        api.block_attn(q, k, k, ids, 64, 32, ws=q.view(torch.uint8).flatten())
+    with pytest.raises(ValueError, match="share"):
+        api.block_topk(q, torch.zeros(1, 2, 2, 64), 64, 1, 32, ws=q.view(torch.uint8).flatten())
+    assert not rec.calls
