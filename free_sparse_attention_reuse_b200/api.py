@@ -753,7 +753,9 @@ class KVCache:
         self.k_scale, self.v_scale = (torch.ones((B, Hkv, capacity // BK), device=dev) for _ in range(2))
         self.means = torch.zeros((B, Hkv, capacity // BK, d), device=dev)
         self.kv_len = torch.zeros(B, dtype=torch.int32, device=dev)
-        self._open = None  # bf16 rows of the unfinished last block
+        # bf16 rows of the unfinished last block; held for good, since memory that one call gave back could be handed
+        # out on its stream while the next call still reads it on another
+        self._open = tuple(torch.empty((B, Hkv, BK, d), dtype=torch.bfloat16, device=dev) for _ in range(2))
 
     def append(self, K, V):
         """Add K, V (bf16 [B, Hkv, n, d]) behind the rows held so far."""
@@ -765,15 +767,19 @@ class KVCache:
         _spec(V, "V", torch.bfloat16, shape)
         if self.length + n > self.capacity:
             raise ValueError(f"{n} more rows do not fit: {self.length} of {self.capacity} are held")
+        if n == 0:
+            return
         tail = self.length % self.BK
         if tail:
-            K, V = (torch.cat([o, x], 2) for o, x in zip(self._open, (K, V)))
+            K, V = (torch.cat([o[:, :, :tail], x], 2) for o, x in zip(self._open, (K, V)))
         cache_write(K, V, self.K8, self.V8, self.k_scale, self.v_scale, self.BK, start=self.length - tail,
                     means=self.means)
         self.length += n
         self.kv_len.fill_(self.length)
         tail = self.length % self.BK
-        self._open = tuple(x[:, :, x.shape[2] - tail:].clone() for x in (K, V)) if tail else None
+        if tail:
+            for o, x in zip(self._open, (K, V)):
+                o[:, :, :tail].copy_(x[:, :, x.shape[2] - tail:])
 
     def attend(self, Q, C: int = 128, kb=None, R=None, want_lse: bool = False, scale=None):
         """(out, lse) of block_attn over the rows held; kb blocks per query block, or all of them."""

@@ -135,3 +135,26 @@ def test_outputs_apart_from_each_other(rec):
     with pytest.raises(ValueError, match="share"):
         api.block_topk(q, torch.zeros(1, 2, 2, 64), 64, 1, 32, ws=q.view(torch.uint8).flatten())
     assert not rec.calls
+
+
+def test_open_rows_stay_in_their_memory(rec):
+    """What append() keeps between calls, which may come on different streams, is never freed or moved; the rows
+    handed to the store are the unfinished block's and the new ones."""
+    c = api.KVCache(1, 2, 256, 64, BK=32, device="cpu")
+    held = lambda: {t.data_ptr() for t in vars(c).values() if isinstance(t, torch.Tensor)} | {  # noqa: E731
+        t.data_ptr() for t in c._open}
+    memory = held()
+    rows = torch.arange(1, 101).bfloat16()[None, None, :, None].expand(1, 2, 100, 64).contiguous()
+    at = 0
+    for n in (5, 0, 1, 40, 18, 32, 3):
+        c.append(rows[:, :, at:at + n].contiguous(), -rows[:, :, at:at + n].contiguous())
+        at += n
+        if n:
+            _, args = rec.calls[-1]
+            first = (at - n) // 32 * 32
+            assert args[4] == first and args[0].N == at - first
+        assert c.length == at and held() == memory and int(c.kv_len[0]) == at
+        tail = at % 32
+        assert torch.equal(c._open[0][:, :, :tail], rows[:, :, at - tail:at])
+        assert torch.equal(c._open[1][:, :, :tail], -rows[:, :, at - tail:at])
+    assert len(rec.calls) == 6

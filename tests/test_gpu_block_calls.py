@@ -167,3 +167,28 @@ def test_logits_far_apart(size, d, C, Nq, fp8):
     ids = torch.arange(Nk // BK, dtype=torch.int32).expand(1, 2, -(-Nq // C), -1).contiguous()
     attn(q, k, v, ids, C, BK, fp8=fp8, scale=1.0)
     api.sync_status()
+
+
+def test_cache_grown_on_two_streams():
+    """append() on one stream and then on the other, each ordered behind the one before, while both keep allocating:
+    the store is that of one stream."""
+    B, H, d, BK, n = 1, 2, 64, 32, 90
+    k, v = rnd(270, B, H, n, d).to(DEV), rnd(271, B, H, n, d).to(DEV)
+    one, two = api.KVCache(B, H, 96, d, BK=BK), api.KVCache(B, H, 96, d, BK=BK)
+    one.append(k, v)
+    steps = [(k[:, :, i:i + 1].contiguous(), v[:, :, i:i + 1].contiguous()) for i in range(n)]
+    side = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i, (x, y) in enumerate(steps):
+        me, other = side[i % 2], side[1 - i % 2]
+        me.wait_stream(other)
+        with torch.cuda.stream(me):
+            two.append(x, y)
+        with torch.cuda.stream(other):
+            torch.full((B, H, BK, d), 1e3, dtype=torch.bfloat16, device=DEV)
+    torch.cuda.synchronize()
+    api.sync_status()
+    for a, b in ((one.K8, two.K8), (one.V8, two.V8)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert torch.equal(one.k_scale, two.k_scale) and torch.equal(one.means, two.means)
+    assert torch.equal(one.kv_len, two.kv_len)
