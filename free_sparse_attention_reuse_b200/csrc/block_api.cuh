@@ -52,7 +52,7 @@ bool shares(const Span& a, std::initializer_list<Span> others) {
 bool block_rows_ok(int BK) { return BK == 32 || BK == 64 || BK == 128; }
 bool query_rows_ok(int C) { return C == 1 || C == 16 || C == 64 || C == 128; }
 
-// Opt-in shared memory of the block-sparse kernels, once per device.
+// Opt-in shared memory, once per device and for the operator that is called.
 template <int HD, bool KV8, bool PAIR>
 bool block_attn_attrs() {
   // the kernel moves registers between its warpgroups and counts on 128 a thread at launch: a build
@@ -69,14 +69,23 @@ bool block_token_attrs() {
   return cudaFuncSetAttribute(block_token_kernel<HD, KV8, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess &&
          cudaFuncSetAttribute(block_token_kernel<HD, KV8, 16>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
 }
-mcs_status block_device(DeviceInfo** out) {
+mcs_status topk_device(DeviceInfo** out) {
+  mcs_status e = current_device(out);
+  if (e != MCS_OK) return e;
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (!(*out)->topk_attrs_set) {
+    if (cudaFuncSetAttribute(block_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTopkMaxBlocks * 8) != cudaSuccess)
+      return MCS_ERR_CUDA;
+    (*out)->topk_attrs_set = true;
+  }
+  return MCS_OK;
+}
+mcs_status block_attn_device(DeviceInfo** out) {
   mcs_status e = current_device(out);
   if (e != MCS_OK) return e;
   std::lock_guard<std::mutex> lock(g_mu);
   if (!(*out)->block_attrs_set) {
-    const int topk = kTopkMaxBlocks * 8;
-    if (cudaFuncSetAttribute(block_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, topk) != cudaSuccess ||
-        !block_token_attrs<64, false>() || !block_token_attrs<64, true>() || !block_token_attrs<128, false>() ||
+    if (!block_token_attrs<64, false>() || !block_token_attrs<64, true>() || !block_token_attrs<128, false>() ||
         !block_token_attrs<128, true>() || !block_attn_attrs<64, false, false>() || !block_attn_attrs<64, false, true>() ||
         !block_attn_attrs<64, true, false>() || !block_attn_attrs<64, true, true>() ||
         !block_attn_attrs<128, false, false>() || !block_attn_attrs<128, false, true>() ||
@@ -301,7 +310,7 @@ mcs_status mcs_rotary(const mcs_rotary_args* a, const void* q, const void* k, co
   if ((q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight)) || (reinterpret_cast<uintptr_t>(pos) & 3u))
     return MCS_ERR_DTYPE_ALIGN;
   DeviceInfo* di = nullptr;
-  mcs_status e = block_device(&di);
+  mcs_status e = current_device(&di);
   if (e != MCS_OK) return e;
   RotaryParams p{};
   for (int s = 0; s < 3; ++s) {
@@ -364,7 +373,7 @@ mcs_status mcs_block_means(mcs_shape s, const void* X, int BK, const int32_t* le
   if (!X || !means) return MCS_ERR_INVALID_ARG;
   if (!aligned16(X) || !aligned16(means) || (reinterpret_cast<uintptr_t>(len) & 3u)) return MCS_ERR_DTYPE_ALIGN;
   DeviceInfo* di = nullptr;
-  if ((e = block_device(&di)) != MCS_OK) return e;
+  if ((e = current_device(&di)) != MCS_OK) return e;
   launch_means(s.d, static_cast<const __nv_bfloat16*>(X), len, means, s.B, s.H, s.N, BK, static_cast<cudaStream_t>(stream));
   return launch_status();
 }
@@ -388,7 +397,7 @@ mcs_status mcs_block_topk(mcs_block_shape s, const void* Q, const float* means, 
   if (!ws || ws_bytes < mcs_block_topk_workspace_size(s, C, BK)) return MCS_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(ws) & 255u) return MCS_ERR_DTYPE_ALIGN;
   DeviceInfo* di = nullptr;
-  if ((e = block_device(&di)) != MCS_OK) return e;
+  if ((e = topk_device(&di)) != MCS_OK) return e;
   const TopkPlan plan = plan_topk(s, C, BK);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   TopkParams p{};
@@ -444,7 +453,7 @@ mcs_status mcs_cache_write(mcs_shape s, const void* K, const void* V, int BK, in
       return MCS_ERR_INVALID_ARG;
   }
   DeviceInfo* di = nullptr;
-  if ((e = block_device(&di)) != MCS_OK) return e;
+  if ((e = current_device(&di)) != MCS_OK) return e;
   CacheWriteParams p{};
   p.X[0] = static_cast<const __nv_bfloat16*>(K);
   p.X[1] = static_cast<const __nv_bfloat16*>(V);
@@ -504,7 +513,7 @@ mcs_status mcs_block_attn(mcs_block_shape s, const void* Q, const void* K, const
   if (!ws || ws_bytes < mcs_block_attn_workspace_size(s, C, BK, kb)) return MCS_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(ws) & 255u) return MCS_ERR_DTYPE_ALIGN;
   DeviceInfo* di = nullptr;
-  if ((e = block_device(&di)) != MCS_OK) return e;
+  if ((e = block_attn_device(&di)) != MCS_OK) return e;
   BlockAttnParams p{};
   p.Q = static_cast<const __nv_bfloat16*>(Q);
   p.K = K;

@@ -26,7 +26,7 @@ struct DeviceInfo {
   bool supported = false;
   int sms = 0;
   bool attrs_set = false;
-  bool block_attrs_set = false;
+  bool topk_attrs_set = false, block_attrs_set = false;
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mu;

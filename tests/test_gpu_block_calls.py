@@ -1,5 +1,9 @@
 """Block-sparse calls side by side, with odd arguments and at their far ends (needs a B200)."""
 
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -192,3 +196,23 @@ def test_cache_grown_on_two_streams():
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
     assert torch.equal(one.k_scale, two.k_scale) and torch.equal(one.means, two.means)
     assert torch.equal(one.kv_len, two.kv_len)
+
+
+FIRST = {
+    "rotary": "api.rotary(x, x, x, torch.zeros(64, 1, dtype=torch.int32, device='cuda'), (64,))[0]",
+    "topk": "api.block_topk(x, torch.ones(1, 64, 7000, 64, device='cuda'), 1, 3, 32)",  # 56 kB of keys a row
+    "attn": "api.block_attn(x, x, x, torch.zeros(1, 64, 1, 1, dtype=torch.int32, device='cuda'), 128, 32)[0]",
+}
+
+
+@pytest.mark.parametrize("op", FIRST)
+def test_first_call_of_a_process(op):
+    """Each operator makes ready what it needs itself, whichever comes first."""
+    code = ("import torch; from free_sparse_attention_reuse_b200 import api; "
+            "x = torch.ones(1, 64, 64, 64, dtype=torch.bfloat16, device='cuda'); "
+            f"y = {FIRST[op]}; api.sync_status(); print('sum', float(y.double().sum()))")
+    got = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                         cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert got.returncode == 0, got.stderr[-2000:]
+    want = {"rotary": 64.0 ** 3, "topk": 64.0 * 64 * (0 + 1 + 2), "attn": 64.0 ** 3}[op]
+    assert got.stdout.split() == ["sum", str(want)]
