@@ -754,8 +754,13 @@ class KVCache:
         self.means = torch.zeros((B, Hkv, capacity // BK, d), device=dev)
         self.kv_len = torch.zeros(B, dtype=torch.int32, device=dev)
         # bf16 rows of the unfinished last block; held for good, since memory that one call gave back could be handed
-        # out on its stream while the next call still reads it on another
-        self._open = tuple(torch.empty((B, Hkv, BK, d), dtype=torch.bfloat16, device=dev) for _ in range(2))
+        # out on its stream while the next call still reads it on another.  Flat, so that any number of them is
+        # contiguous: as a slice of [B, Hkv, BK, d] they made an append of 1500 rows of 24 heads take 95 us, not 52
+        self._open = tuple(torch.empty(B * Hkv * BK * d, dtype=torch.bfloat16, device=dev) for _ in range(2))
+
+    def _open_rows(self, tail: int):
+        """The first `tail` rows of the unfinished block's keys and values, [B, Hkv, tail, d] each."""
+        return [o[:self.B * self.Hkv * tail * self.d].view(self.B, self.Hkv, tail, self.d) for o in self._open]
 
     def append(self, K, V):
         """Add K, V (bf16 [B, Hkv, n, d]) behind the rows held so far."""
@@ -771,15 +776,15 @@ class KVCache:
             return
         tail = self.length % self.BK
         if tail:
-            K, V = (torch.cat([o[:, :, :tail], x], 2) for o, x in zip(self._open, (K, V)))
+            K, V = (torch.cat([o, x], 2) for o, x in zip(self._open_rows(tail), (K, V)))
         cache_write(K, V, self.K8, self.V8, self.k_scale, self.v_scale, self.BK, start=self.length - tail,
                     means=self.means)
         self.length += n
         self.kv_len.fill_(self.length)
         tail = self.length % self.BK
         if tail:
-            for o, x in zip(self._open, (K, V)):
-                o[:, :, :tail].copy_(x[:, :, x.shape[2] - tail:])
+            for o, x in zip(self._open_rows(tail), (K, V)):
+                o.copy_(x[:, :, x.shape[2] - tail:])
 
     def attend(self, Q, C: int = 128, kb=None, R=None, want_lse: bool = False, scale=None):
         """(out, lse) of block_attn over the rows held; kb blocks per query block, or all of them."""

@@ -155,6 +155,7 @@ def test_open_rows_stay_in_their_memory(rec):
             assert args[4] == first and args[0].N == at - first
         assert c.length == at and held() == memory and int(c.kv_len[0]) == at
         tail = at % 32
-        assert torch.equal(c._open[0][:, :, :tail], rows[:, :, at - tail:at])
-        assert torch.equal(c._open[1][:, :, :tail], -rows[:, :, at - tail:at])
+        k, v = c._open_rows(tail)
+        assert torch.equal(k, rows[:, :, at - tail:at])
+        assert torch.equal(v, -rows[:, :, at - tail:at])
     assert len(rec.calls) == 6
