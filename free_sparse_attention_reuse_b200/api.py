@@ -735,7 +735,7 @@ def cache_write(K, V, K8, V8, k_scale, v_scale, BK: int, start: int = 0, means=N
 class KVCache:
     """Keys and values of one layer in 8 bits, for attention from new frames or tokens to all earlier
     ones: e4m3 values, one scale per block of BK tokens and head, and each block's mean key, which
-    scores the blocks without reading them.
+    scores the blocks without reading them.  All B sequences have one length.
 
     append() adds rows (an unfinished last block keeps its bf16 rows beside the store, so that it is
     quantised anew, with its own scale, whenever it grows); attend() runs attention over every

@@ -119,6 +119,8 @@ BlockPlan plan_block_attn(const mcs_block_shape& s, int C, int BK, int kb, bool 
   // 16 rows 42 | 29, 64 rows 107 | 30; 30 k keys, 16 rows 14 | 20, 64 rows 21 | 21, 128 rows 25 | 22; 2 k keys,
   // 128 rows 11 | 16.  8 bits: 960 k keys, 16 rows 77 | 103, 24 rows 123 | 104; 256 k keys, 16 rows 39 | 37,
   // 24 rows 51 | 37; 30 k keys, 64 rows 20 | 22, 128 rows 29 | 23.
+  // (Lists of 16 rows have no other form: tiles of 128 rows would be an eighth full.  They read their keys once for
+  // 16 rows: a clip of 24 heads, 37 of 252 blocks, 15.8 ms where lists of 128 rows take 2.0.)
   const long long reads = static_cast<long long>(s.B) * s.Hkv * s.Nk * ((q.Nq + 15) / 16);
   q.tensor = listed ? C >= 64 : q.Nq > (kv8 ? 16 : 8) && reads >= 131072;
   q.pair = q.tensor && listed && C == 64;

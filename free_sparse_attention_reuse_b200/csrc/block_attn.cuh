@@ -447,7 +447,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
       }
     } else {
-      // ---- 8-bit tiles, loaded by warp 13, widened to bf16: every warp its run of 32 keys of each
+      // ---- 8-bit tiles, loaded by warp 13, widened (keys to fp16, values to bf16): every warp its run of 32 keys
+      // of each
       constexpr int LPR = HD / 8, RPI = 32 / LPR, NIT = 32 / RPI;  // lanes to a row (8 values each), rows of a pass
       const int sub = lane / LPR, c = lane % LPR;
       constexpr uint32_t RAWS = L::RAWS;
@@ -502,7 +503,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int T = sUnit[u_it & 3].x + sUnit[u_it & 3].y;
         // Q to fp16 in place, a row a thread: times the power of two that brings its largest element into
         // [2^14, 2^15), whose exponent the softmax gets (exact down to 2^-28 of that element, off by at
-        // most 2^-40 of it below)
+        // most 2^-39 of it below; rows under 2^-107 are brought up by 2^121 alone)
         if (!mbar_wait_warp(q_full, u_it & 1, abort_flag, wl)) break;
         const int row = pw * 32 + lane;
         uint32_t top = 0;

@@ -53,9 +53,11 @@ __device__ __forceinline__ void mma_16816_zero(float* d, uint32_t a0, uint32_t a
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-// A row of Q as fp16 fragments: times the power of two that brings its largest element into [2^14, 2^15),
-// which `unscale` takes back.  Exact for elements down to 2^-28 of the largest, off by at most 2^-40 of
-// it below.  (A row with infinities or NaN gives NaN either way.)
+// A row of Q as fp16 fragments: times the power of two that brings its largest element into [2^14, 2^15); returned
+// is the one that takes it back.  Exact for elements down to 2^-28 of the largest, off by at most 2^-39 of
+// it below (half of fp16's 2^-24 steps).  The exponent is kept where both powers are normal numbers: a row whose
+// largest element is below 2^-107 is brought up by 2^121, and its elements are off by at most 2^-146.  (A row with
+// infinities or NaN gives NaN either way.)
 template <int N>
 __device__ __forceinline__ float q_to_f16(uint32_t* q) {
   float top = 0.f;
@@ -66,7 +68,6 @@ __device__ __forceinline__ float q_to_f16(uint32_t* q) {
   }
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  // exponent of the largest element, kept where both powers of two are normal numbers
   const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 20), 254) - 127;
   const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
 #pragma unroll

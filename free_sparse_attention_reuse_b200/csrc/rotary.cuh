@@ -90,7 +90,7 @@ __device__ __forceinline__ void load_w4(const void* w, int bf16, size_t at, floa
 // heads (through a share of them where there are more groups than tokens), kRotRows rows in flight.  With
 // pairs in halves a lane holds four elements of the first half and their four partners (two 8-byte
 // pieces), so that nothing is exchanged; lanes beyond the halves hold eight that are not turned.
-// Bound: device memory (480p clip, head norm: 196 us, 92 % of the copy rate; one row in flight and the sines
+// Bound: device memory (480p clip, head norm: 198 us, 91 % of the copy rate; one row in flight and the sines
 // in shared memory left it at 58 %; partners by shuffles left the halves form at 143 us for 403 MB,
 // three CTAs an SM instead of four at 117 against 105, five at 137).
 template <int HD, int NORM, bool HALVES>

@@ -259,8 +259,9 @@ typedef struct {
  *                  token's heads, weight [heads, d]; w = 1 where the weight is NULL),
  *                  then pair i turns by pos[axis(i)] * theta^(-2 j / axis_dim), j its place in its axis's
  *                  section: (x1 cos - x2 sin, x1 sin + x2 cos).  Elements behind the axes' sum do not turn.
- *   v is copied.  k and K, v and V may be NULL together.  Outputs must not alias inputs.
- * All in fp32 (angles in fp64), rounded once. */
+ *   v is copied.  k and K, v and V may be NULL together.  Outputs must not alias inputs or each other.
+ * All in fp32 (angles in fp64), rounded once; a norm's squares are fp32 too, so elements of 2^55 and more, or an
+ * rms under 2^-60 without an eps, are outside its range. */
 mcs_status mcs_rotary(const mcs_rotary_args* a, const void* q, const void* k, const void* v, const void* pos,
                       const void* q_weight, const void* k_weight, void* Q, void* K, void* V, void* stream);
 
@@ -294,7 +295,10 @@ mcs_status mcs_cache_write(mcs_shape s, const void* K, const void* V, int BK, in
  * skipped; a block listed twice counts twice); blocks = NULL: every block, kb = nb.
  * lse[b,h,i] (nullable, fp32) = log sum_j exp(scale q_i . k_j).  A row without a key: out = R (0 without R),
  * lse = -inf.  kv_format 0: K, V bf16, no scales; 1: e4m3 with k_scale, v_scale fp32 [B, Hkv, nb] (positive
- * and finite, as mcs_cache_write makes them), Nk a multiple of BK.  R nullable; out must not alias an input. */
+ * and finite, as mcs_cache_write makes them), Nk a multiple of BK.  R nullable; out and lse must not alias an input
+ * or each other.  Probabilities are bf16 (relative 2^-8), before normalisation up to 2^32 where later keys lie above
+ * the first ones, so values should stay below 2^90.  e4m3 keys with lists of 1 or 16 rows, or a whole store and few
+ * rows: fp16 (relative 2^-11 down to 2^-29 of the row's largest, off by at most 2^-40 of it below). */
 size_t mcs_block_attn_workspace_size(mcs_block_shape s, int C, int BK, int kb);
 mcs_status mcs_block_attn(mcs_block_shape s, const void* Q, const void* K, const void* V, int kv_format,
                           const float* k_scale, const float* v_scale, const int32_t* blocks, int C, int BK, int kb,
