@@ -216,3 +216,50 @@ def test_first_call_of_a_process(op):
     assert got.returncode == 0, got.stderr[-2000:]
     want = {"rotary": 64.0 ** 3, "topk": 64.0 * 64 * (0 + 1 + 2), "attn": 64.0 ** 3}[op]
     assert got.stdout.split() == ["sum", str(want)]
+
+
+@pytest.mark.parametrize("d,BK,C", [(64, 64, 64), (128, 128, 128), (128, 32, 16), (64, 32, 1)])
+def test_whole_path_captured(d, BK, C):
+    """Rotary, the store, the choice and the attention in one graph, replayed on other data and on another stream,
+    and beside an eager run: what the calls give one after the other."""
+    B, H, Hkv, n, cap, kb = 2, 4, 2, 150, 512, 3
+    axes, start = (16, 24, 24), 2 * BK
+    x = [torch.empty(B, n, m, d, dtype=torch.bfloat16, device=DEV) for m in (H, Hkv, Hkv)]
+    pos = torch.empty(B, n, 3, dtype=torch.int32, device=DEV)
+    kv, lens = torch.empty(B, dtype=torch.int32, device=DEV), torch.empty(B, dtype=torch.int32, device=DEV)
+
+    def store():
+        e = lambda: torch.zeros(B, Hkv, cap, d, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)  # noqa: E731
+        s = lambda *t: torch.ones(B, Hkv, cap // BK, *t, device=DEV)  # noqa: E731
+        return e(), e(), s(), s(), s(d)
+
+    def path(K8, V8, ks, vs, mk):
+        Q, K, V = api.rotary(*x, pos, axes, norm="head")
+        api.cache_write(K, V, K8, V8, ks, vs, BK, start=start, means=mk, lens=lens)
+        ids = api.block_topk(Q, mk, C, kb, BK, kv_len=kv)
+        out, lse = api.block_attn(Q, K8, V8, ids, C, BK, kv_len=kv, k_scale=ks, v_scale=vs, want_lse=True)
+        return out, lse, ids, K8.view(torch.uint8), V8.view(torch.uint8), ks, vs, mk
+
+    def fill(seed):
+        for i, t in enumerate(x):
+            t.copy_(rnd(seed + i, *t.shape))
+        pos.copy_(torch.randint(0, 1000, pos.shape, generator=torch.Generator().manual_seed(seed)))
+        lens.copy_(torch.tensor([n, n - seed % 97]))
+        kv.copy_(start + lens)
+
+    fill(300)
+    mine, theirs = store(), store()
+    path(*store())
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        got = path(*mine)
+    for seed in (310, 320, 333):
+        fill(seed)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            graph.replay()
+        want = path(*theirs)  # beside it
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    api.sync_status()
